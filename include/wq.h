@@ -69,7 +69,8 @@ typedef enum wq_status {
   WQ_ERR_TIMEOUT = 8,     /* device: a bounded barrier wait gave up              */
   WQ_ERR_RANGE = 9,       /* device: a code given to wq_pack_int4 exceeds 15, or */
                           /* a factor s_j given to wq_quantize_rtn_scaled is not */
-                          /* finite and > 0                                       */
+                          /* finite and > 0, or a length, slot or block given to  */
+                          /* a wq_kv4_ call does not fit                          */
   WQ_ERR_NODEVICE = 10,   /* no CUDA device, or it is not sm_100                 */
   WQ_ERR_DEVICE = 11      /* a pointer is not memory of the current device      */
 } wq_status;
@@ -261,6 +262,115 @@ wq_status wq_quantize_gptq(const void* W, wq_dtype w_dtype, int64_t N, int64_t K
                            const uint16_t* X, int64_t T, int64_t ldx, double damp,
                            const wq_qparams* params, uint8_t* packed, uint16_t* S, uint16_t* Z,
                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- 4-bit KV cache: the same round-to-nearest group-wise affine INT4 ("DL S067 -
+ * Quantization", sections 1-2), applied to the keys and values of attention. A cache is made of blocks of
+ * block_size tokens; a request's block table lists the blocks that hold its tokens in order,
+ * and a slot is block * block_size + token within the block. Keys and values of a token are
+ * quantized per head in groups along the head dimension, with S' and Z exactly as
+ * wq_quantize_rtn_g128 gives them for a row; everything below computes with S'(q - Z).
+ *
+ * Memory: wq_kv4_cache_bytes(cache) bytes, 16-byte aligned, [num_blocks][kv_heads] chunks of
+ * block_size * (head_dim + 8 * head_dim / group) bytes, no initial contents required: what a
+ * request's length does not reach is never used, whatever it holds. The order of the bytes in
+ * a chunk is the library's own (wq_kv4_append writes it, wq_kv4_read gives values back).
+ * Supported: head_dim 64 or 128; group 32, 64 or 128, at most head_dim; block_size 16, 32, 64,
+ * 128 or 256 (else WQ_ERR_UNSUPPORTED); num_blocks * block_size < 2^31. */
+typedef struct wq_kv4_cache {
+  void* data;
+  int64_t num_blocks;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t group;
+  int32_t block_size;
+} wq_kv4_cache;
+
+/* Bytes of a cache (data is not looked at); 0 for an unsupported description. */
+size_t wq_kv4_cache_bytes(const wq_kv4_cache* cache);
+
+/* Block tables and slot map of one step, from the requests' lengths, in one launch. Request b
+ * holds ctx_lens[b] tokens already and gets new_lens[b] more. New blocks are taken from
+ * free_blocks[0 ..] in the order of the requests, ceil((ctx + new)/block_size) -
+ * ceil(ctx/block_size) each, and entered into row b of tables [B, width] (row stride
+ * ld_tables) behind those it has; other entries are left as they are. Outputs:
+ *   slots [n_slots]   slot of every new token, requests one after the other; -1 behind the
+ *                     last (n_slots may be a padded batch's size)
+ *   q_starts [B + 1]  first new token of each request, and their number
+ *   kv_lens [B]       ctx + new
+ *   taken [1]         number of free blocks used
+ * The call reads only ctx_lens, new_lens, free_blocks and the entries of held blocks, so that
+ * it can be repeated and captured. WQ_ERR_RANGE in the status word: a negative length (that
+ * request counts as empty), a table row or free_blocks too short, a held block that is
+ * negative (the tokens concerned get slot -1), or more tokens than n_slots. int32 arrays,
+ * 4-byte aligned; no array may overlap another. */
+wq_status wq_kv4_block_tables(const int32_t* ctx_lens, const int32_t* new_lens, int64_t B,
+                              const int32_t* free_blocks, int64_t n_free, int32_t block_size,
+                              int32_t* tables, int64_t width, int64_t ld_tables, int32_t* slots,
+                              int64_t n_slots, int32_t* q_starts, int32_t* kv_lens,
+                              int32_t* taken, void* stream);
+
+/* Quantize and store the keys and values of T tokens: K, V [T, kv_heads, head_dim] bf16 or
+ * fp16 with the given strides in elements (unit stride along head_dim), token t into
+ * slots[t]. A negative slot is skipped; a slot beyond the cache is skipped and sets
+ * WQ_ERR_RANGE. A group that is not finite, or whose scale passes binary16, is stored as
+ * zeros and sets WQ_ERR_NONFINITE. Slots >= 0 must differ from one another (else the doubled
+ * slot holds a mixture of its tokens). K, V 16-byte aligned, strides multiples of 8. */
+wq_status wq_kv4_append(const uint16_t* K, const uint16_t* V, wq_dtype dtype, int64_t T,
+                        int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                        int64_t v_head_stride, const int32_t* slots, const wq_kv4_cache* cache,
+                        void* stream);
+
+/* Stored values S'(q - Z) of T slots into K, V [T, kv_heads, head_dim], contiguous: WQ_F32
+ * exact, WQ_BF16 and WQ_F16 rounded once (half to even). A negative slot gives zeros; a slot
+ * beyond the cache zeros and WQ_ERR_RANGE. K, V 16-byte aligned. */
+wq_status wq_kv4_read(const wq_kv4_cache* cache, const int32_t* slots, int64_t T, void* K,
+                      void* V, wq_dtype out_dtype, void* stream);
+
+/* Attention of new tokens over the cache, for single tokens, drafted tokens and prompts.
+ * Rows q_starts[b] .. q_starts[b+1] - 1 of Q [T, heads, head_dim] are the last tokens of
+ * request b, whose kv_lens[b] tokens (these included, appended before the call) lie in the
+ * blocks of row b of tables [B, width] (row stride ld_tables). Query head h reads KV head
+ * h / (heads / kv_heads). With n the number of the request's rows, row i
+ * sees key j for j <= kv_lens[b] - n + i (causal != 0) or j < kv_lens[b] (causal == 0), and,
+ * with window > 0, only the last `window` of those.
+ *   out = sum_j softmax_j(scale q . k_j) v_j,  [T, heads, head_dim] in Q's type
+ *   lse = ln sum_j exp(scale q . k_j), [T, heads] float32, contiguous; may be NULL
+ * A row that sees no key gives out = 0 and lse = -inf. Rows of Q outside q_starts are not
+ * read, and their out and lse are left as they were. Scores, softmax statistics and sums are
+ * fp32; probabilities are rounded once to binary16 (2^-12 relative) before they meet the
+ * values, and out once to its type. The result is deterministic. max_q should be the largest
+ * number of rows of a request: it chooses kernels, and a wrong one costs time only.
+ * Strides in elements, unit along head_dim, multiples of 8; Q, out, workspace 16-byte
+ * aligned; Q and out bf16 or fp16. The workspace needs no initial contents; calls that may
+ * run at the same time need one each. WQ_ERR_RANGE in the status word: a table entry outside
+ * the cache, or a length beyond the table, where it is needed (those keys are left out). */
+typedef struct wq_kv4_attention_args {
+  const uint16_t* Q;
+  int64_t T;
+  int64_t q_token_stride;
+  int64_t q_head_stride;
+  wq_kv4_cache cache;
+  const int32_t* tables;
+  int64_t width;
+  int64_t ld_tables;
+  const int32_t* q_starts;
+  const int32_t* kv_lens;
+  int64_t B;
+  uint16_t* out;
+  int64_t o_token_stride;
+  int64_t o_head_stride;
+  float* lse;
+  void* workspace;
+  uint64_t workspace_bytes;
+  int32_t dtype; /* wq_dtype of Q and out */
+  int32_t heads;
+  int32_t max_q;
+  int32_t causal;
+  int32_t window; /* 0: none; at most 2^30 */
+  float scale;
+} wq_kv4_attention_args;
+size_t wq_kv4_attention_workspace_bytes(void);
+wq_status wq_kv4_attention(const wq_kv4_attention_args* args, void* stream);
 
 /* Synchronize `stream`, then return and clear the current device's status word:
  * WQ_OK, or the first of WQ_ERR_NONFINITE / WQ_ERR_RANGE / WQ_ERR_TIMEOUT recorded by a

@@ -5,3 +5,4 @@ TEST INFRASTRUCTURE ONLY. Only ``tests/``, ``__graft_entry__.smoke()`` and the
 The CUDA library never calls it, and it shares no code with the CUDA library.
 """
 from .wq_oracle import *  # noqa: F401,F403
+from .kv4_oracle import *  # noqa: F401,F403

@@ -1,0 +1,512 @@
+"""The 4-bit KV cache on a GPU against the float64 oracle: block tables and slot maps (equal),
+append and read (bit for bit, the cache's bytes included), and attention within the bound that
+the oracle derives for it, for single tokens, drafts and prompts; rows that see nothing, stale
+and uninitialised memory, bad pages, strides, graphs, streams and a run of the operators
+together."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import oracle  # noqa: E402
+import w4a16_dequant_matmul_b200 as wq  # noqa: E402
+
+DEV = "cuda"
+BF16, F16 = torch.bfloat16, torch.float16
+RANGE, NONFINITE = 9, 7
+
+
+def ints(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device=DEV)
+
+
+def ok():
+    assert wq.wq_get_status() == 0
+
+
+# ------------------------------------------------------------------------- block tables
+
+def tables_case(ctx, new, block, extra_slots=0, extra_width=1, seed=0):
+    rng = np.random.default_rng(seed)
+    held = [-(-c // block) for c in ctx]
+    need = [-(-(c + n) // block) for c, n in zip(ctx, new)]
+    pool = rng.permutation(sum(need) + 3)
+    tab = np.full((len(ctx), max(need + [0]) + extra_width), -7)
+    at = 0
+    for b, n in enumerate(held):
+        tab[b, :n] = pool[at: at + n]
+        at += n
+    return tab, pool[at:], sum(new) + extra_slots
+
+
+@pytest.mark.parametrize("ctx,new,block,extra", [
+    ([0], [1], 16, 0), ([0], [0], 16, 3), ([15], [1], 16, 0), ([16], [1], 16, 0), ([31, 0, 5], [1, 1, 1], 32, 2),
+    ([0, 0, 0, 0], [0, 17, 0, 64], 64, 5), ([100], [1000], 128, 1), ([1000], [513], 256, 0)])
+def test_block_tables_small(ctx, new, block, extra):
+    tab, free, n = tables_case(ctx, new, block, extra)
+    want = oracle.kv4_block_tables(ctx, new, free, tab, block, n)
+    got = ints(tab)
+    slots, starts, kv, taken = wq.wq_kv4_block_tables(ints(ctx), ints(new), ints(free), got, block, n)
+    ok()
+    for g, w in zip((got, slots, starts, kv, taken), want):
+        assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
+
+
+@pytest.mark.parametrize("requests", [511, 512, 513, 1500])
+@pytest.mark.parametrize("most", [1, 40])
+def test_block_tables_many(requests, most):
+    rng = np.random.default_rng(requests + most)
+    ctx, new = rng.integers(0, 300, requests), rng.integers(0, most + 1, requests)
+    tab, free, n = tables_case(ctx.tolist(), new.tolist(), 16, 11, 2, seed=requests)
+    want = oracle.kv4_block_tables(ctx.tolist(), new.tolist(), free, tab, 16, n)
+    wide = torch.full((requests, tab.shape[1] + 5), -9, dtype=torch.int32, device=DEV)
+    got = wide[:, : tab.shape[1]]  # rows with a stride of their own
+    got.copy_(ints(tab))
+    for _ in range(2):  # repeating the call changes nothing
+        out = wq.wq_kv4_block_tables(ints(ctx), ints(new), ints(free), got, 16, n)
+        for g, w in zip((got, *out), want):
+            assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
+    assert bool((wide[:, tab.shape[1]:] == -9).all())
+    ok()
+
+
+def test_block_tables_errors():
+    """Each shortage is reported in the status word, the tokens concerned get slot -1 and what
+    fits is right."""
+    tab = ints(np.full((2, 2), -1))
+    slots, *_ = wq.wq_kv4_block_tables(ints([0, 0]), ints([20, 20]), ints([5, 6, 7]), tab, 16, 40)
+    assert wq.wq_get_status() == RANGE  # the fourth block is missing
+    s = slots.cpu().numpy()
+    assert (s[:36] >= 0).all() and (s[36:] == -1).all() and tab.cpu().tolist() == [[5, 6], [7, -1]]
+    slots, starts, kv, taken = wq.wq_kv4_block_tables(ints([0]), ints([40]), ints([5, 6, 7]), ints([[-1, -1]]), 16, 40)
+    assert wq.wq_get_status() == RANGE and (slots[32:] == -1).all() and kv.item() == 40  # width 2
+    slots, *_ = wq.wq_kv4_block_tables(ints([3]), ints([2]), ints([1]), ints([[-1]]), 16, 2)
+    assert wq.wq_get_status() == RANGE and (slots == -1).all()  # the held block is missing
+    slots, starts, kv, taken = wq.wq_kv4_block_tables(ints([-4, 0]), ints([2, 2]), ints([3]), ints([[-1], [-1]]), 16, 4)
+    assert wq.wq_get_status() == RANGE and starts.tolist() == [0, 0, 2] and kv.tolist() == [0, 2]
+    assert slots.tolist() == [48, 49, -1, -1]
+    slots, *_ = wq.wq_kv4_block_tables(ints([0]), ints([5]), ints([2]), ints([[-1]]), 16, 3)
+    assert wq.wq_get_status() == RANGE and slots.tolist() == [32, 33, 34]  # more tokens than slots
+    slots, starts, kv, taken = wq.wq_kv4_block_tables(ints([]), ints([]), ints([]), torch.empty(0, 0, dtype=torch.int32, device=DEV), 16, 2)
+    assert slots.tolist() == [-1, -1] and starts.tolist() == [0] and taken.item() == 0
+    ok()
+
+
+# ---------------------------------------------------------------------- append and read
+
+def quantized(x, group):
+    """Oracle codes, S, Z of x [T, H, D] (float64 values)."""
+    T, H, D = x.shape
+    q, s, z = oracle.quantize_rtn_asym(x.reshape(-1, D), group)
+    return q.reshape(x.shape), s.reshape(T, H, -1), z.reshape(T, H, -1)
+
+
+def rows(T, H, D, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, H, D, generator=g, dtype=torch.float64) * (1 + 5 * (torch.rand(H, D, generator=g) < 0.05))
+    x[0] = 0.0                      # S' = 0 -> 1
+    if T > 3:
+        x[1] = x[1].abs() + 0.25    # one-signed
+        x[2] = torch.arange(D) - D // 2  # ties
+        x[3] *= 1e-6                # subnormal scales
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("block,T,H", [(16, 37, 3), (64, 70, 1), (256, 5, 2)])
+def test_append_and_read(dim, group, dtype, block, T, H):
+    k, v = rows(T, H, dim, dtype, 1), rows(T, H, dim, dtype, 2)
+    blocks = -(-T // block) + 2
+    rng = np.random.default_rng(T)
+    slots = rng.permutation(blocks * block)[:T]
+    slots[T // 2] = -1
+    slots[-1] = -5
+    cache = wq.wq_kv4_alloc(blocks, H, dim, group, block)
+    cache.fill_(0xA5)
+    want = cache.cpu().numpy().copy()
+    kq, vq = quantized(k.double().numpy(), group), quantized(v.double().numpy(), group)
+    oracle.kv4_pack_cache(want, slots, kq, vq, block)
+    wq.wq_kv4_append(k.to(DEV), v.to(DEV), ints(slots), cache, group=group)
+    ok()
+    assert np.array_equal(cache.cpu().numpy(), want), "cache bytes"
+    live = (slots >= 0)[:, None, None]
+    for out_dtype in (torch.float32, BF16, F16):
+        got = wq.wq_kv4_read(cache, ints(slots), dim, group=group, out_dtype=out_dtype)
+        ok()
+        for x, (q, s, z) in zip(got, (kq, vq)):
+            exact = (s[..., None] * (q.reshape(T, H, -1, group) - z[..., None])).reshape(T, H, dim) * live
+            assert torch.equal(x.cpu(), torch.from_numpy(exact).float().to(out_dtype))
+
+
+def test_append_strided():
+    """K and V as slices of a fused projection's output, heads in another order in memory."""
+    T, H, D = 19, 4, 64
+    x = torch.randn(T, 3 * H * D, device=DEV).to(BF16)
+    k = x[:, H * D: 2 * H * D].unflatten(-1, (H, D))
+    v = torch.randn(H, T, D, device=DEV).to(BF16).transpose(0, 1)
+    slots = ints(np.arange(T) + 3)
+    a, b = wq.wq_kv4_alloc(2, H, D, 32, 16), wq.wq_kv4_alloc(2, H, D, 32, 16)
+    a.zero_(), b.zero_()
+    wq.wq_kv4_append(k, v, slots, a, group=32)
+    wq.wq_kv4_append(k.contiguous(), v.contiguous(), slots, b, group=32)
+    assert torch.equal(a, b) and bool(a.any())
+    ok()
+
+
+def test_append_reports_bad_input():
+    cache = wq.wq_kv4_alloc(2, 1, 64, 32, 16)
+    cache.zero_()
+    k = torch.ones(3, 1, 64, device=DEV, dtype=BF16)
+    bad = k.clone()
+    bad[1, 0, 40] = float("nan")
+    bad[2, 0, 3] = float("inf")
+    wq.wq_kv4_append(bad, k, ints([0, 1, 2]), cache, group=32)
+    assert wq.wq_get_status() == NONFINITE
+    got, _ = wq.wq_kv4_read(cache, ints([0, 1, 2]), 64, group=32)
+    one = 15 * float(np.float16(1 / 15))  # S' q of a row of ones
+    assert bool((got[1, 0, :32] == one).all()) and not bool(got[1, 0, 32:].any()) and not bool(got[2, 0, :32].any())
+    before = cache.clone()
+    wq.wq_kv4_append(k, k, ints([32, -1, 1 << 30]), cache, group=32)  # 32 slots: 0 .. 31
+    assert wq.wq_get_status() == RANGE and torch.equal(cache, before)
+    got, _ = wq.wq_kv4_read(cache, ints([32, -1, 0]), 64, group=32)
+    assert wq.wq_get_status() == RANGE and not bool(got[:2].any()) and bool(got[2].all())
+    huge = torch.full((1, 1, 64), 1e30, device=DEV, dtype=BF16)  # S' passes binary16
+    wq.wq_kv4_append(huge, huge, ints([5]), cache, group=32)
+    assert wq.wq_get_status() == NONFINITE
+
+
+def test_slots_past_32_bits_of_bytes():
+    """A cache of more than 2^32 bytes: its last blocks are written and read."""
+    blocks = (1 << 32) // (16 * 8 * 136) + 100
+    cache = wq.wq_kv4_alloc(blocks, 8, 128, 128, 16)
+    assert cache.numel() > 1 << 32
+    T = 7
+    k, v = rows(T, 8, 128, BF16, 3), rows(T, 8, 128, BF16, 4)
+    slots = ints(np.arange(T) + (blocks - 1) * 16 + 4)
+    wq.wq_kv4_append(k.to(DEV), v.to(DEV), slots, cache)
+    got = wq.wq_kv4_read(cache, slots, 128)
+    ok()
+    for x, w in zip(got, (k, v)):
+        q, s, z = quantized(w.double().numpy(), 128)
+        assert np.array_equal(x.double().cpu().numpy(), s * (q - z))
+    table = torch.full((1, 1), blocks - 1, dtype=torch.int32, device=DEV)
+    q = torch.randn(1, 8, 128, device=DEV).to(BF16)
+    small = cache[blocks - 1:].clone()
+    a = wq.wq_kv4_attention(q, cache, table, ints([0, 1]), ints([9]), 1)
+    b = wq.wq_kv4_attention(q, small, table * 0, ints([0, 1]), ints([9]), 1)
+    ok()
+    assert torch.equal(a, b)
+
+
+# --------------------------------------------------------------------------- attention
+
+class Case:
+    """A cache with quantized random keys and values, everything else in it hostile: stale
+    blocks and the tails of the last ones hold random bytes, their scales NaN and infinities."""
+
+    def __init__(self, kv_lens, q_lens, heads, kv_heads, dim, group, block, dtype, seed=0, spread=1.0):
+        rng = np.random.default_rng(seed)
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        self.kv_lens, self.q_lens, self.dim, self.group, self.dtype = kv_lens, q_lens, dim, group, dtype
+        need = [-(-n // block) for n in kv_lens]
+        blocks = sum(need) + 2
+        self.cache = wq.wq_kv4_alloc(blocks, kv_heads, dim, group, block)
+        self.cache.copy_(torch.randint(0, 256, self.cache.shape, generator=g, device=DEV, dtype=torch.uint8))
+        half = block * dim
+        self.cache[..., half:].view(torch.float16)[...] = float("nan")
+        self.cache[..., half::8] = 0
+        order, at = rng.permutation(blocks), 0
+        tab = np.full((len(kv_lens), max(need + [1]) + 1), -1)
+        self.k, self.v, self.smax = [], [], []
+        for b, n in enumerate(need):
+            tab[b, :n] = order[at: at + n]
+            at += n
+            m = kv_lens[b]
+            slots = ints([tab[b, j // block] * block + j % block for j in range(m)])
+            k = (torch.randn(m, kv_heads, dim, generator=g, device=DEV) * spread).to(dtype)
+            v = (torch.randn(m, kv_heads, dim, generator=g, device=DEV) * (0.1 + torch.rand(m, kv_heads, 1, generator=g, device=DEV) * 3)).to(dtype)
+            wq.wq_kv4_append(k, v, slots, self.cache, group=group)
+            kk, vv = wq.wq_kv4_read(self.cache, slots, dim, group=group)
+            self.k.append(kk.double().cpu().numpy())
+            self.v.append(vv.double().cpu().numpy())
+            x = k.float().unflatten(-1, (-1, group))
+            span = (x.amax(-1).clamp(min=0) - x.amin(-1).clamp(max=0)) / 15 * (1 + 2.0**-11)
+            self.smax.append(float(span.max()) if m else 0.0)
+        self.tables, self.kv = ints(tab), ints(kv_lens)
+        self.starts = ints(np.concatenate(([0], np.cumsum(q_lens))))
+        T = sum(q_lens)
+        self.q = torch.randn(T, heads, dim, generator=g, device=DEV).to(dtype)
+        ok()
+
+    def run(self, **kw):
+        kw = {"causal": True, "window": 0, **kw}
+        max_q = kw.pop("max_q", max(self.q_lens + [1]))
+        return wq.wq_kv4_attention(self.q, self.cache, self.tables, self.starts, self.kv, max_q, group=self.group, return_lse=True, **kw)
+
+    def check(self, out, lse, scale=None, causal=True, window=0):
+        scale = self.dim ** -0.5 if scale is None else scale
+        half_step = torch.finfo(self.dtype).eps / 2
+        tiny = float(torch.finfo(self.dtype).smallest_normal) * half_step
+        at = 0
+        for b, n in enumerate(self.q_lens):
+            q = self.q[at: at + n].double().cpu().numpy()
+            want, wlse, bound, blse = oracle.kv4_attention(q, self.k[b], self.v[b], scale, causal, window, s_max=self.smax[b])
+            got = out[at: at + n].double().cpu().numpy()
+            gl = lse[at: at + n].double().cpu().numpy()
+            limit = bound + (np.abs(want) + bound) * half_step + tiny
+            assert np.isfinite(got).all()
+            worst = np.max((np.abs(got - want) - limit).ravel(), initial=-1)
+            assert worst <= 0, f"request {b}: {np.max(np.abs(got - want) / (limit + 1e-300)):.3g} of the bound"
+            assert np.array_equal(np.isneginf(gl), np.isneginf(wlse))
+            f = np.isfinite(wlse)
+            assert (np.abs(gl[f] - wlse[f]) <= blse[f]).all(), f"lse of request {b}"
+            at += n
+
+
+SHAPES = [(128, 128), (128, 64), (128, 32), (64, 64), (64, 32)]
+
+
+@pytest.mark.parametrize("dim,group", SHAPES)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_decode_one_token(dim, group, dtype):
+    for kv in (1, 2, 15, 16, 17, 63, 64, 65, 300):
+        c = Case([kv], [1], 8, 2, dim, group, 16, dtype, seed=kv)
+        c.check(*c.run())
+        ok()
+
+
+@pytest.mark.parametrize("dim,group", SHAPES)
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (3, 3), (7, 1), (8, 1), (9, 1), (16, 1), (33, 3), (40, 2)])
+def test_decode_head_layouts(dim, group, heads, kv_heads):
+    c = Case([77, 0, 130], [1, 1, 1], heads, kv_heads, dim, group, 32, BF16, seed=heads)
+    c.check(*c.run())
+    ok()
+
+
+@pytest.mark.parametrize("block", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("dim,group", [(128, 128), (64, 32)])
+def test_decode_ragged_batch(block, dim, group):
+    """Lengths of all kinds, an empty place among them; pages end inside a tile."""
+    c = Case([0, 1, 257, 64, 1000, 31, 128, 513], [1] * 8, 8, 2, dim, group, block, BF16, seed=block)
+    c.check(*c.run())
+    ok()
+
+
+@pytest.mark.parametrize("q_lens", [[1, 0, 2, 5], [3, 3, 3, 3], [8, 1, 30, 2]])
+@pytest.mark.parametrize("dim,group,dtype", [(128, 128, BF16), (128, 32, F16), (64, 64, F16)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 7), (True, 100), (False, 0), (False, 33)])
+def test_drafts(q_lens, dim, group, dtype, causal, window):
+    """Several queries a request, the first of them before its keys where a request is short."""
+    c = Case([200, 3, 1, 66], q_lens, 12, 4, dim, group, 16, dtype, seed=sum(q_lens))
+    c.check(*c.run(causal=causal, window=window), causal=causal, window=window)
+    ok()
+
+
+@pytest.mark.parametrize("dim,group,dtype", [(128, 128, BF16), (128, 128, F16), (128, 64, BF16), (64, 64, BF16), (64, 32, F16)])
+@pytest.mark.parametrize("q_lens,kv_lens", [([130], [130]), ([64, 1, 0, 200], [64, 300, 5, 333]), ([129], [700]), ([50, 33], [20, 33])])
+@pytest.mark.parametrize("heads,kv_heads", [(4, 4), (8, 2), (7, 1)])
+def test_prompts(dim, group, dtype, q_lens, kv_lens, heads, kv_heads):
+    c = Case(kv_lens, q_lens, heads, kv_heads, dim, group, 32, dtype, seed=heads)
+    c.check(*c.run())
+    ok()
+
+
+@pytest.mark.parametrize("causal,window", [(True, 1), (True, 65), (False, 0), (False, 50)])
+@pytest.mark.parametrize("block", [16, 64, 128])
+def test_prompt_masks(causal, window, block):
+    c = Case([140, 300], [140, 90], 8, 2, 128, 128, block, BF16, seed=block)
+    c.check(*c.run(causal=causal, window=window), causal=causal, window=window)
+    ok()
+
+
+def test_scales_and_sharp_softmax():
+    """Scores of hundreds (the running maximum moves far and often), a scale of 0 (the mean of
+    the values), a negative one."""
+    for scale, spread in ((0.5, 4.0), (0.0, 1.0), (-0.1, 1.0)):
+        for q_lens in ([1, 2], [40, 1]):
+            c = Case([400, 90], q_lens, 8, 2, 128, 128, 16, BF16, seed=5, spread=spread)
+            c.check(*c.run(scale=scale), scale=scale)
+    ok()
+
+
+def test_far_apart_value_scales():
+    """Values whose scales lie 2^20 apart: a token of weight near 1 with tiny values beside
+    ones of little weight with large values."""
+    c = Case([130], [1], 4, 1, 64, 64, 16, F16, seed=9)
+    v = torch.randn(130, 1, 64, device=DEV) * torch.exp2(torch.randint(-14, 7, (130, 1, 1), device=DEV).float())
+    k = torch.randn(130, 1, 64, device=DEV)
+    slots = c.tables[0].long()[torch.arange(130, device=DEV) // 16] * 16 + torch.arange(130, device=DEV) % 16
+    wq.wq_kv4_append(k.half(), v.half(), slots.int(), c.cache, group=64)
+    kk, vv = wq.wq_kv4_read(c.cache, slots.int(), 64, group=64)
+    c.k, c.v = [kk.double().cpu().numpy()], [vv.double().cpu().numpy()]
+    c.smax = [float((k.half().float().amax(-1).clamp(min=0) - k.half().float().amin(-1).clamp(max=0)).max()) / 15 * 1.001]
+    c.check(*c.run())
+    ok()
+
+
+def test_long_context_split_over_the_grid():
+    """One request whose keys are spread over every CTA, against torch in float64."""
+    kv, heads, kv_heads, dim = 40000, 8, 1, 128
+    cache = wq.wq_kv4_alloc(kv // 64 + 1, kv_heads, dim)
+    k, v = torch.randn(2, kv, kv_heads, dim, device=DEV).to(BF16).unbind(0)
+    slots = torch.arange(kv, device=DEV, dtype=torch.int32)
+    wq.wq_kv4_append(k, v, slots, cache)
+    kk, vv = wq.wq_kv4_read(cache, slots, dim)
+    q = torch.randn(1, heads, dim, device=DEV).to(BF16)
+    table = torch.arange(cache.shape[0], device=DEV, dtype=torch.int32)[None]
+    out, lse = wq.wq_kv4_attention(q, cache, table, ints([0, 1]), ints([kv]), 1, return_lse=True)
+    ok()
+    s = torch.einsum("hd,kd->hk", q[0].double(), kk[:, 0].double()) * dim**-0.5
+    p = torch.softmax(s, 1)
+    want = p @ vv[:, 0].double()
+    # rounding of p 2^-12, of out 2^-8, sums and scores as in the oracle's bound (kv/16 steps)
+    size = p @ vv[:, 0].double().abs()
+    limit = size * (2.0**-12 + 2.0**-14 + kv / 16 * 2.0**-23) + want.abs() * 2.0**-8
+    assert bool(((out[0].double() - want).abs() <= limit).all())
+    assert torch.allclose(lse[0].double(), torch.logsumexp(s, 1), rtol=0, atol=1e-4)
+    again = wq.wq_kv4_attention(q, cache, table, ints([0, 1]), ints([kv]), 1)
+    assert torch.equal(out, again), "deterministic"
+
+
+def test_bad_pages_and_lengths():
+    """Table entries outside the cache and lengths beyond the table: reported, those keys left
+    out, the rest right, other requests untouched."""
+    for q_lens in ([1, 1, 1], [40, 1, 1]):
+        c = Case([100, 90, 50], q_lens, 4, 2, 128, 128, 16, BF16, seed=3)
+        good = c.run()
+        ok()
+        tab = c.tables.clone()
+        tab[1, 2], tab[1, 4] = -1, 1 << 20
+        keep = c.tables
+        c.tables = tab
+        out, lse = c.run()
+        assert wq.wq_get_status() == RANGE
+        n = q_lens[0]
+        assert torch.equal(out[:n], good[0][:n]) and torch.equal(out[n + 1:], good[0][n + 1:])
+        seen = np.r_[0:32, 48:64, 80:90]
+        s = np.einsum("hd,khd->hk", c.q[n].double().cpu().numpy(), np.repeat(c.k[1][seen], 2, 1)) * 128**-0.5
+        p = np.exp(s - s.max(1, keepdims=True))
+        want = np.einsum("hk,khd->hd", p / p.sum(1, keepdims=True), np.repeat(c.v[1][seen], 2, 1))
+        assert np.abs(out[n].double().cpu().numpy() - want).max() < 2.0**-7 * np.abs(want).max()
+        c.tables = keep[:, :2].contiguous()  # 32 tokens
+        out, lse = c.run()
+        assert wq.wq_get_status() == RANGE and bool(torch.isfinite(out).all())
+
+
+def test_rows_behind_the_last_are_left():
+    for q_lens in ([1, 2], [60, 1]):
+        c = Case([90, 33], q_lens, 4, 2, 64, 64, 16, F16, seed=1)
+        T = sum(q_lens)
+        q = torch.cat((c.q, torch.full((5, 4, 64), float("nan"), device=DEV, dtype=F16)))
+        out = torch.full((T + 5, 4, 64), 7.0, device=DEV, dtype=F16)
+        got, lse = wq.wq_kv4_attention(q, c.cache, c.tables, c.starts, c.kv, max(q_lens), group=64, out=out, return_lse=True)
+        ok()
+        assert got is out and bool((out[T:] == 7).all())
+        c.check(out[:T], lse[:T])
+
+
+def test_strided_queries_and_outputs():
+    for q_lens in ([2, 1], [70, 3]):
+        c = Case([90, 33], q_lens, 4, 2, 128, 128, 16, BF16, seed=2)
+        T = sum(q_lens)
+        wide = torch.zeros(T, 6, 136, device=DEV, dtype=BF16)
+        wide[:, 1:5, :128] = c.q
+        out = torch.zeros(4, T, 256, device=DEV, dtype=BF16)
+        view = out.transpose(0, 1)[..., 128:]
+        got = wq.wq_kv4_attention(wide[:, 1:5, :128], c.cache, c.tables, c.starts, c.kv, max(q_lens), out=view)
+        ok()
+        assert torch.equal(got, c.run()[0]) and not bool(out[..., :128].any())
+
+
+def test_a_wrong_max_q_changes_no_result():
+    c = Case([300, 90, 64], [80, 1, 20], 8, 2, 128, 128, 32, BF16, seed=4)
+    for max_q in (0, 1, 80, 5000):
+        c.check(*c.run(max_q=max_q))
+    ok()
+
+
+def test_many_requests():
+    """More requests than threads of a CTA."""
+    rng = np.random.default_rng(0)
+    kv = rng.integers(0, 70, 700).tolist()
+    c = Case(kv, [1] * 700, 2, 1, 64, 64, 16, BF16, seed=11)
+    out, lse = c.run()
+    ok()
+    c.check(out, lse)
+
+
+def test_graph_streams_and_workspaces():
+    """Captured and replayed with other contents; two streams with a workspace each; one
+    workspace for two graphs that run one after the other."""
+    c = Case([500, 70, 128], [1, 1, 1], 8, 2, 128, 128, 16, BF16, seed=6)
+    c.run()
+    ws = torch.full((wq.wq_kv4_attention_workspace_bytes(),), 0xFF, dtype=torch.uint8, device=DEV)
+    out1, out2 = torch.zeros_like(c.q), torch.zeros_like(c.q)
+    q2 = c.q * 2
+    graphs = []
+    for q, out in ((c.q, out1), (q2, out2)):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            wq.wq_kv4_attention(q, c.cache, c.tables, c.starts, c.kv, 1, out=out, workspace=ws)
+        graphs.append(g)
+    want2 = wq.wq_kv4_attention(q2, c.cache, c.tables, c.starts, c.kv, 1)
+    for _ in range(3):
+        out1.zero_(), out2.zero_()
+        for g in graphs:
+            g.replay()
+        assert torch.equal(out1, c.run()[0]) and torch.equal(out2, want2)
+    # other lengths and contents in the same buffers
+    c.kv.copy_(ints([200, 0, 17]))
+    graphs[0].replay()
+    c.kv_lens, c.k, c.v = [200, 0, 17], [x[:n] for x, n in zip(c.k, (200, 0, 17))], [x[:n] for x, n in zip(c.v, (200, 0, 17))]
+    c.check(out1, c.run()[1])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(c.run()[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    ok()
+
+
+def test_a_serving_run():
+    """The operators as they are used together: prompts are admitted, appended and attended,
+    then tokens are decoded one by one, a prompt joining in between; each step's attention
+    against the oracle on what the cache holds by then."""
+    heads, kv_heads, dim, block, budget = 8, 2, 128, 16, 64
+    cache = wq.wq_kv4_alloc(40, kv_heads, dim, dim, block)
+    tables = torch.full((3, 12), -1, dtype=torch.int32, device=DEV)
+    free = torch.from_numpy(np.random.default_rng(0).permutation(40)).int().to(DEV)
+    ctx, held = np.zeros(3, int), [[np.zeros((0, kv_heads, dim))] * 2 for _ in range(3)]
+    used = 0
+    g = torch.Generator(device=DEV).manual_seed(0)
+    for new in ([37, 0, 20], [1, 0, 1], [1, 50, 1], [1, 1, 1], [1, 1, 0], [1, 1, 1]):
+        n = sum(new)
+        slots, starts, kv, taken = wq.wq_kv4_block_tables(ints(ctx), ints(new), free[used:], tables, block, budget)
+        q = torch.randn(budget, heads, dim, generator=g, device=DEV).to(BF16)
+        k, v = torch.randn(2, budget, kv_heads, dim, generator=g, device=DEV).to(BF16).unbind(0)
+        wq.wq_kv4_append(k, v, slots, cache)
+        out, lse = wq.wq_kv4_attention(q, cache, tables, starts, kv, max(new), return_lse=True)
+        ok()
+        used += taken.item()
+        kq, vq = quantized(k[:n].double().cpu().numpy(), dim), quantized(v[:n].double().cpu().numpy(), dim)
+        kk, vv = (x[1] * (x[0] - x[2]) for x in (kq, vq))
+        at = 0
+        for b in range(3):
+            held[b] = [np.concatenate((old, x[at: at + new[b]])) for old, x in zip(held[b], (kk, vv))]
+            want, wl, bound, bl = oracle.kv4_attention(q[at: at + new[b]].double().cpu().numpy(), *held[b], dim**-0.5, s_max=1.0)
+            got = out[at: at + new[b]].double().cpu().numpy()
+            assert (np.abs(got - want) <= bound + (np.abs(want) + bound) * 2.0**-8).all()
+            assert (np.abs(lse[at: at + new[b]].double().cpu().numpy() - wl) <= bl).all()
+            at += new[b]
+        ctx += np.array(new)
+    assert kv.tolist() == ctx.tolist()

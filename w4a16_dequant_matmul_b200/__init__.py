@@ -18,6 +18,12 @@ Functions carry the C names:
     wq_quantize_rtn_scaled(W, s, group=128, zero_point=True) -> (packed, S, Z)
     wq_scale_activations(X, s) -> X / s
     wq_quantize_gptq(W, X, group=128, zero_point=True, damp=0.01) -> (packed, S, Z)
+    wq_kv4_alloc(num_blocks, kv_heads, head_dim, group, block_size) -> cache
+    wq_kv4_block_tables(ctx_lens, new_lens, free_blocks, tables, block_size, n_slots)
+        -> (slots, q_starts, kv_lens, taken)
+    wq_kv4_append(K, V, slots, cache, group)
+    wq_kv4_read(cache, slots, head_dim, group, out_dtype) -> (K, V)
+    wq_kv4_attention(Q, cache, tables, q_starts, kv_lens, max_q, group, ...) -> out
     wq_get_status() -> int
 S and Z are returned as torch.float16 tensors (binary16 bit patterns in the C ABI).
 """
@@ -26,6 +32,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 from ._build import LIB_PATH, build_library  # noqa: F401  (build_library re-exported)
 
@@ -37,6 +44,8 @@ __all__ = [
     "wq_w8a16_gemm", "wq_get_status", "wq_selftest_bounded_wait",
     "wq_channel_stat", "wq_smooth_scales", "wq_awq_scales", "wq_quantize_rtn_scaled",
     "wq_scale_activations", "wq_quantize_gptq", "wq_gptq_workspace_bytes",
+    "wq_kv4_alloc", "wq_kv4_cache_bytes", "wq_kv4_block_tables", "wq_kv4_append",
+    "wq_kv4_read", "wq_kv4_attention", "wq_kv4_attention_workspace_bytes",
     "WQ_F32", "WQ_BF16", "WQ_F16", "WQ_U8", "WQ_I8", "WQ_STAT_ABSMAX", "WQ_STAT_ABSMEAN",
 ]
 
@@ -59,6 +68,10 @@ class _QParams(ctypes.Structure):
     _fields_ = [("w_bit", ctypes.c_int32), ("group", ctypes.c_int32),
                 ("zero_point", ctypes.c_int32)]
 
+
+# wq_kv4_cache and wq_kv4_attention_args, packed in one call each (the decode hot path)
+_KV4_CACHE = struct.Struct("Pqiiii")
+_KV4_ATTENTION = struct.Struct("PqqqPqiiiiPqqPPqPqqPPQiiiiif")
 
 _LIB = None
 _P = ctypes.c_void_p
@@ -89,6 +102,14 @@ _SIGNATURES = {
     "wq_quantize_gptq": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _I64, _I64, ctypes.c_double,
                                 ctypes.POINTER(_QParams), _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "wq_selftest_bounded_wait": (_I32, [ctypes.c_uint64, _I32, _P]),
+    "wq_kv4_cache_bytes": (ctypes.c_size_t, [ctypes.c_char_p]),
+    "wq_kv4_block_tables": (_I32, [_P, _P, _I64, _P, _I64, _I32, _P, _I64, _I64, _P, _I64, _P,
+                                   _P, _P, _P]),
+    "wq_kv4_append": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _I64, _I64, _P, ctypes.c_char_p,
+                             _P]),
+    "wq_kv4_read": (_I32, [ctypes.c_char_p, _P, _I64, _P, _P, _I32, _P]),
+    "wq_kv4_attention_workspace_bytes": (ctypes.c_size_t, []),
+    "wq_kv4_attention": (_I32, [ctypes.c_char_p, _P]),
 }
 
 
@@ -452,6 +473,184 @@ def wq_quantize_gptq(W, X, group: int = 128, zero_point: bool = True, damp: floa
                                     _stream(stream))
     _check(st, "wq_quantize_gptq")
     return packed, S, Z
+
+
+_KV4_DTYPES = None
+
+
+def _kv4_dtype(t, name):
+    global _KV4_DTYPES
+    if _KV4_DTYPES is None:
+        import torch
+
+        _KV4_DTYPES = {torch.bfloat16: WQ_BF16, torch.float16: WQ_F16}
+    code = _KV4_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float16")
+    return code
+
+
+def _kv4_ints(t, name, shape):
+    """A contiguous int32 tensor of the given shape (None: any size)."""
+    if str(t.dtype) != "torch.int32":
+        raise TypeError(f"{name} must be int32")
+    got = tuple(t.shape)
+    if len(got) != len(shape) or any(w is not None and w != n for n, w in zip(got, shape)):
+        raise ValueError(f"{name} has shape {got}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _kv4_heads(t, name):
+    """(tokens, heads, head_dim, token stride, head stride) of a [T, heads, head_dim] tensor."""
+    n, h, d = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name} must have unit stride along head_dim")
+    return n, h, d, st if n > 1 else 0, sh if h > 1 else 0
+
+
+def _kv4_cache(cache, head_dim, group):
+    """(packed wq_kv4_cache, its fields, group) of a cache tensor of wq_kv4_alloc."""
+    group = head_dim if group is None else group
+    if str(cache.dtype) != "torch.uint8" or cache.dim() != 3 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 [num_blocks, kv_heads, bytes] tensor")
+    n, h, chunk = cache.shape
+    row = head_dim + 8 * (head_dim // group) if group > 0 else 0
+    if row <= 0 or chunk % row:
+        raise ValueError(f"a cache with {chunk} bytes a chunk is not one of head_dim {head_dim}, "
+                         f"group {group}")
+    return cache.data_ptr(), n, h, head_dim, group, chunk // row
+
+
+def wq_kv4_cache_bytes(num_blocks: int, kv_heads: int, head_dim: int, group: int = None,
+                       block_size: int = 64) -> int:
+    """Bytes of a 4-bit KV cache; 0 if the description is not supported."""
+    group = head_dim if group is None else group
+    return int(lib().wq_kv4_cache_bytes(
+        _KV4_CACHE.pack(0, num_blocks, kv_heads, head_dim, group, block_size)))
+
+
+def wq_kv4_alloc(num_blocks: int, kv_heads: int, head_dim: int, group: int = None,
+                 block_size: int = 64, device="cuda"):
+    """Memory of a 4-bit KV cache: uint8 [num_blocks, kv_heads, bytes of a block of a head], not
+    initialised. group defaults to head_dim (one scale a row)."""
+    import torch
+
+    one = wq_kv4_cache_bytes(1, kv_heads, head_dim, group, block_size)
+    if one == 0 or (num_blocks > 0 and wq_kv4_cache_bytes(num_blocks, kv_heads, head_dim, group,
+                                                          block_size) == 0):
+        raise WQError(5, "wq_kv4_alloc")
+    return torch.empty((num_blocks, kv_heads, one // kv_heads), dtype=torch.uint8, device=device)
+
+
+def wq_kv4_block_tables(ctx_lens, new_lens, free_blocks, tables, block_size: int, n_slots: int,
+                        stream=None):
+    """Block tables and slot map of one step: enters the blocks that the requests' new tokens
+    need, taken from free_blocks in order, into `tables` (int32 [B, width], in place) and
+    returns (slots int32 [n_slots], q_starts int32 [B + 1], kv_lens int32 [B], taken int32 [1]).
+    ctx_lens, new_lens: int32 [B], tokens held and tokens to come. Slots behind the last new
+    token are -1."""
+    import torch
+
+    B = ctx_lens.shape[0]
+    _kv4_ints(ctx_lens, "ctx_lens", (B,))
+    _kv4_ints(new_lens, "new_lens", (B,))
+    _kv4_ints(free_blocks, "free_blocks", (None,))
+    if tables.dtype != torch.int32 or tables.dim() != 2 or tables.shape[0] != B:
+        raise ValueError("tables must be int32 [B, width]")
+    ld = _rows(tables, "tables")
+    out = torch.empty((n_slots + 2 * B + 2,), dtype=torch.int32, device=ctx_lens.device)
+    slots, q_starts, kv_lens, taken = out.split((n_slots, B + 1, B, 1))
+    with _on_device(ctx_lens):
+        st = lib().wq_kv4_block_tables(
+            ctx_lens.data_ptr(), new_lens.data_ptr(), B, free_blocks.data_ptr(),
+            free_blocks.shape[0], block_size, tables.data_ptr(), tables.shape[1], ld,
+            slots.data_ptr(), n_slots, q_starts.data_ptr(), kv_lens.data_ptr(), taken.data_ptr(),
+            _stream_handle(ctx_lens, stream))
+    _check(st, "wq_kv4_block_tables")
+    return slots, q_starts, kv_lens, taken
+
+
+def wq_kv4_append(K, V, slots, cache, group: int = None, stream=None) -> None:
+    """Quantize keys and values [T, kv_heads, head_dim] (bfloat16 or float16, any token and head
+    strides) into slots (int32 [T], negative: skipped) of the cache."""
+    T, h, d, kt, kh = _kv4_heads(K, "K")
+    if V.shape != K.shape or V.dtype != K.dtype:
+        raise ValueError("K and V must have one shape and dtype")
+    _, _, _, vt, vh = _kv4_heads(V, "V")
+    _kv4_ints(slots, "slots", (T,))
+    c = _kv4_cache(cache, d, group)
+    if c[2] != h:
+        raise ValueError(f"the cache has {c[2]} KV heads, K has {h}")
+    with _on_device(K):
+        st = lib().wq_kv4_append(K.data_ptr(), V.data_ptr(), _kv4_dtype(K, "K"), T, kt, kh, vt, vh,
+                                 slots.data_ptr(), _KV4_CACHE.pack(*c), _stream_handle(K, stream))
+    _check(st, "wq_kv4_append")
+
+
+def wq_kv4_read(cache, slots, head_dim: int, group: int = None, out_dtype=None, stream=None):
+    """Values S'(q - Z) stored in slots (int32 [T]; zeros for negative ones): (K, V), each
+    [T, kv_heads, head_dim] float32 (exact), bfloat16 or float16."""
+    import torch
+
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    code = {torch.float32: WQ_F32, torch.bfloat16: WQ_BF16, torch.float16: WQ_F16}.get(out_dtype, -1)
+    _kv4_ints(slots, "slots", (None,))
+    c = _kv4_cache(cache, head_dim, group)
+    T = slots.shape[0]
+    K, V = torch.empty((2, T, c[2], head_dim), dtype=out_dtype, device=cache.device).unbind(0)
+    with _on_device(cache):
+        st = lib().wq_kv4_read(_KV4_CACHE.pack(*c), slots.data_ptr(), T, K.data_ptr(), V.data_ptr(),
+                               code, _stream_handle(cache, stream))
+    _check(st, "wq_kv4_read")
+    return K, V
+
+
+def wq_kv4_attention_workspace_bytes() -> int:
+    return int(lib().wq_kv4_attention_workspace_bytes())
+
+
+def wq_kv4_attention(Q, cache, tables, q_starts, kv_lens, max_q: int, group: int = None,
+                     scale: float = None, causal: bool = True, window: int = 0, out=None,
+                     return_lse: bool = False, workspace=None, stream=None):
+    """Attention of Q [T, heads, head_dim] (bfloat16 or float16) over the cache: rows
+    q_starts[b] .. q_starts[b + 1] - 1 are the last tokens of request b, whose kv_lens[b] tokens
+    lie in the blocks of tables[b]. Returns out (Q's shape and type), or (out, lse float32
+    [T, heads]). scale defaults to head_dim ** -0.5; max_q: the largest number of rows of a
+    request; window > 0: each row sees the last `window` keys only. Rows outside q_starts are
+    left as they were."""
+    import torch
+
+    T, heads, d, qt, qh = _kv4_heads(Q, "Q")
+    c = _kv4_cache(cache, d, group)
+    B = kv_lens.shape[0]
+    _kv4_ints(kv_lens, "kv_lens", (B,))
+    _kv4_ints(q_starts, "q_starts", (B + 1,))
+    if tables.dtype != torch.int32 or tables.dim() != 2 or tables.shape[0] != B:
+        raise ValueError("tables must be int32 [B, width]")
+    if out is None:
+        out = torch.empty((T, heads, d), dtype=Q.dtype, device=Q.device)
+        ot, oh = heads * d, d
+    else:
+        if out.shape != Q.shape or out.dtype != Q.dtype:
+            raise ValueError("out must have Q's shape and dtype")
+        _, _, _, ot, oh = _kv4_heads(out, "out")
+    lse = torch.empty((T, heads), dtype=torch.float32, device=Q.device) if return_lse else None
+    if workspace is None:
+        workspace = torch.empty((wq_kv4_attention_workspace_bytes(),), dtype=torch.uint8,
+                                device=Q.device)
+    args = _KV4_ATTENTION.pack(
+        Q.data_ptr(), T, qt, qh, *c, tables.data_ptr(), tables.shape[1], _rows(tables, "tables"),
+        q_starts.data_ptr(), kv_lens.data_ptr(), B, out.data_ptr(), ot, oh,
+        0 if lse is None else lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _kv4_dtype(Q, "Q"), heads, int(max_q),
+        1 if causal else 0, int(window), d ** -0.5 if scale is None else float(scale))
+    with _on_device(Q):
+        st = lib().wq_kv4_attention(args, _stream_handle(Q, stream))
+    if st != 0:
+        raise WQError(st, "wq_kv4_attention")
+    return (out, lse) if return_lse else out
 
 
 def wq_selftest_bounded_wait(limit_ns: int = 20_000_000, spin: bool = True, stream=None) -> None:

@@ -106,7 +106,9 @@ const char* wq_status_string(wq_status s) {
     case WQ_ERR_CUDA: return "CUDA runtime error";
     case WQ_ERR_NONFINITE: return "non-finite weight or scale overflow";
     case WQ_ERR_TIMEOUT: return "device wait timed out";
-    case WQ_ERR_RANGE: return "code above 15, or a scale factor not finite and positive";
+    case WQ_ERR_RANGE:
+      return "code above 15, a scale factor not finite and positive, or a KV length, slot or "
+             "block out of range";
     case WQ_ERR_NODEVICE: return "no usable sm_100 CUDA device";
     case WQ_ERR_DEVICE: return "a pointer is not memory of the current device";
   }
