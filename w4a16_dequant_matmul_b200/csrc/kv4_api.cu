@@ -190,9 +190,19 @@ wq_status wq_kv4_attention(const wq_kv4_attention_args* p, void* stream) {
   a.out = p->out;
   a.lse = p->lse;
   a.workspace = p->workspace;
-  a.most_rows = static_cast<int>(kIntMax);
   a.status = status;
-  return from_cuda(wq::launch_kv4_decode(a, p->max_q, sms, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Where some request may have more rows than the decode kernel takes in one pass, the prompt
+  // kernel gets those requests and the decode kernel the others; which are which is read on
+  // the device. A single request needs no such split.
+  a.most_rows = static_cast<int>(kIntMax);
+  if (wq::kv4_prompt_ok(a) &&
+      static_cast<int64_t>(p->max_q) * a.ratio > wq::kKv4DecodeRows) {
+    a.most_rows = a.requests == 1 ? 0 : wq::kKv4DecodeRows;
+    const wq_status e = from_cuda(wq::launch_kv4_prompt(a, st));
+    if (e != WQ_OK || a.requests == 1) return e;
+  }
+  return from_cuda(wq::launch_kv4_decode(a, p->max_q, sms, st));
 }
 
 }  // extern "C"
