@@ -62,19 +62,22 @@ def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None):
     bound_out, bound_lse): the formula's values, and how far a kernel may be from them before
     its output is rounded.
 
-    The bound. A kernel's score is an fp32 sum of D/16 steps of 16 exact products
-    x (16 + q_code) S scale with 16 + q_code <= 31, minus x-sum (16 + Z) S scale: each step and
-    each of about 8 further fp32 operations errs by at most 2^-23 of the largest magnitude in
-    it, at most 31 S scale sum|x| (`s_max`: the largest S of the request's keys). That makes
-    every probability wrong by a relative e = (D/16 + 8) 2^-23 31 S scale sum|x| at most, and
-    numerator and denominator by e each; with it 2^-12 for its rounding to binary16 (half a
-    step of 2^-11), 2^-20 for exp2, log2 and the scale products, and (kv/16 + 64) 2^-23 for the
-    two fp32 sums over the keys. The error of out is that times sum_j p_j |v_j|, and where p is
-    a binary16 subnormal half its step, 2^-25: the weights p_j S_j are lifted so that the
-    largest is 2^7 at least, a key's codes less Z are 15 at most, so the keys together err by
-    at most kv 15 2^-32 max_j(p_j S_j) / l, and 15 S_j <= 2.2 max_d |v_j| (the range 15 S lies
-    within twice the largest stored value, each end of it within S/2). For a masked row all of
-    it is 0."""
+    The bound. A kernel's score is an fp32 sum of D/8 steps at most, of 16 exact products
+    x (16 + q_code) S scale with 16 + q_code <= 31, minus x-sum (16 + Z) S scale, or of the
+    products with both 16-bit parts of S (q - Z): each step and each of about 8 further fp32
+    operations errs by at most 2^-23 of the largest magnitude in it, at most 31 S scale sum|x|
+    (`s_max`: the largest S of the request's keys); a binary16 part of S (q - Z) / 16 may be a
+    subnormal, half a step of 2^-24 off. That makes every probability wrong by a relative
+        e = ((D/8 + 8) 2^-23 31 S + 2^-21) scale sum|x|
+    at most, and numerator and denominator by e each; with it 2^-12 for its rounding to binary16
+    (half a step of 2^-11) and 2^-12 for that of its value, 2^-20 for exp2, log2 and the scale
+    products, and (kv/16 + 64) 2^-23 for the two fp32 sums over the keys. The error of out is
+    that times sum_j p_j |v_j|. Where a rounded p is a binary16 subnormal it errs by half its
+    step, 2^-25, with the largest p at 2^6 at least (or the largest p S, then a key's codes
+    less Z are 15 at most): 2^-31 max|v| of every key, where 15 S <= 2.2 max_d |v_j| (the range
+    15 S lies within twice the largest stored value, each end of it within S/2). Where a
+    rounded value is one, it errs by 2^-25 with the largest S at 2^4 at least: 2^-29 S. For a
+    masked row all of it is 0."""
     n, heads, dim = q.shape
     kv, kv_heads = k.shape[0], k.shape[1]
     out = np.zeros((n, heads, dim))
@@ -97,9 +100,9 @@ def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None):
             lse[i, h] = m + np.log(l)
             e = 0.0
             if s_max is not None:
-                e = (dim / 16 + 8) * 2.0**-23 * 31 * s_max * abs(scale) * np.abs(q[i, h]).sum()
-            rel = 2 * e + 2.0**-12 + 2.0**-20 + (kv / 16 + 64) * 2.0**-23
-            low = (last + 1 - first) * 2.0**-32 * 2.2 * np.max(p * np.abs(vv).max(1)) / l
+                e = ((dim / 8 + 8) * 2.0**-23 * 31 * s_max + 2.0**-21) * abs(scale) * np.abs(q[i, h]).sum()
+            rel = 2 * e + 2.0**-11 + 2.0**-20 + (kv / 16 + 64) * 2.0**-23
+            low = ((last + 1 - first) * 2.0**-31 / l + 2.0**-29) * 2.2 * np.abs(vv).max()
             bound[i, h] = rel * (p @ np.abs(vv) / l) + low
             bound_lse[i, h] = e + 2.0**-20 * (1 + abs(lse[i, h])) + (kv / 16 + 64) * 2.0**-23
     return out, lse, bound, bound_lse

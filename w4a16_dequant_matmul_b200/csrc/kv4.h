@@ -97,9 +97,8 @@ struct Kv4AttnArgs {
 size_t kv4_decode_workspace_bytes(int sms);
 cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int max_q, int sms, cudaStream_t st);
 
-// Requests with more rows than a.most_rows, on tcgen05 (one group a row).
+// Requests with more rows than a.most_rows, on tcgen05.
 constexpr int kKv4DecodeRows = 16;
-bool kv4_prompt_ok(const Kv4AttnArgs& a);
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs& a, cudaStream_t st);
 
 }  // namespace wq

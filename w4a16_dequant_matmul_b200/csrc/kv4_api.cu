@@ -196,8 +196,7 @@ wq_status wq_kv4_attention(const wq_kv4_attention_args* p, void* stream) {
   // kernel gets those requests and the decode kernel the others; which are which is read on
   // the device. A single request needs no such split.
   a.most_rows = static_cast<int>(kIntMax);
-  if (wq::kv4_prompt_ok(a) &&
-      static_cast<int64_t>(p->max_q) * a.ratio > wq::kKv4DecodeRows) {
+  if (static_cast<int64_t>(p->max_q) * a.ratio > wq::kKv4DecodeRows) {
     a.most_rows = a.requests == 1 ? 0 : wq::kKv4DecodeRows;
     const wq_status e = from_cuda(wq::launch_kv4_prompt(a, st));
     if (e != WQ_OK || a.requests == 1) return e;

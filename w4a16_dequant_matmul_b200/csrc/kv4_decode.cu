@@ -637,10 +637,12 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->empty[s]);
       }
-      // a timeout in any warp ends the unit for all of them (the barriers below need all four)
-      named_barrier(1, 32 * kWarps);
-      if (ctl->abort) ok = false;
-      if (!ok) break;
+      // a timeout in any warp ends the work of all four (the barriers below need them all, so
+      // they have to decide alike)
+      if (named_barrier_or(1, 32 * kWarps, !ok)) {
+        ok = false;
+        break;
+      }
 
       // ---------------------------------------------------- join the four warps' states
 #pragma unroll

@@ -3,14 +3,21 @@
 //
 // A CTA (one per SM) takes 256 rows of one (request, KV head), as two tiles of 128, against
 // tiles of 128 keys:
-//     S_i = Q_i C_k^T        tcgen05.mma, both operands in shared memory, S_i in TMEM
-//     p   = 2^(S_i ks + lv - m + 7),  l += p / S_v
-//     O_i += P_i C_v         P_i (binary16) from TMEM, O_i in TMEM
-// C_k, C_v are the codes less their Z, exact in 16 bits: a key's scale meets its score in fp32
-// (ks = S_k scale log2(e)), a value's joins the exponent (lv = log2 S_v), so that no operand
-// is rounded but p. A key outside the request has lv = -inf. One thread owns a row: it reads
-// its 128 scores from TMEM, and m moves (which rescales O_i in TMEM) only when a score passes
-// it by 2^8; the scores are read again then.
+//     S_i = Q_i K^T          tcgen05.mma, both operands in shared memory, S_i in TMEM
+//     p   = 2^(S_i ks - m + 6),  l += p
+//     O_i += P_i V           P_i (binary16) from TMEM, O_i in TMEM
+// Where a key's row has one scale, K is its codes less Z, exact in 16 bits, and the scale meets
+// the score in fp32 (ks = S_k scale log2(e)). With several, K is S_k (q - Z) as a sum of two
+// 16-bit numbers (15 bits in all, so the sum is exact) and the product runs twice; ks is then
+// one number. For bf16 results V is S_v (q - Z) 2^-E rounded once to binary16 (2^-12, under the
+// rounding of out by 2^3); for fp16 results that would show, so V stays exact: with one scale
+// the codes less Z, S_v 2^-E meeting p, with several a sum of two numbers as for K. E is the
+// exponent of the largest S_v so far: one number for all rows, which moves rarely (O is
+// rescaled then), so values of any magnitude keep their bits.
+// One thread owns a row: it reads its 128 scores from TMEM, and m moves (which rescales O_i in
+// TMEM) only when a score passes it by 2^8; the scores are read again then. Of the constants of
+// a key only ks comes from shared memory for every score: the loads of three of them (scale,
+// logarithm and reciprocal of S_v) bounded an earlier form, 3.6 us a step of 128 keys.
 //
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (and Q's load, the output); 8-11 expand: codes
 // straight from global memory, one tile ahead in registers, into the two-deep rings of K
@@ -36,7 +43,7 @@ constexpr int kN = 128;       // keys of a tile
 constexpr int kRowsCta = 2 * kM;
 constexpr int kThreads = 512;
 constexpr uint64_t kLimitNs = 2000000000ull;
-constexpr float kLift = 7.0f, kHeadroom = 8.0f;
+constexpr float kLift = 6.0f, kHeadroom = 8.0f;  // p <= 2^14
 
 // Registers of a thread after the split: the launch gives every warpgroup 128, and the four
 // shares add up to the same.
@@ -57,19 +64,29 @@ struct Ctl {
   uint64_t v_full[2], v_empty[2];
   uint64_t vec_full[4];
   uint64_t s_full[2], p_full[2];
+  uint64_t w_full;  // the expand warps have written wmax
   uint64_t o_full;
   int64_t scan[16];
+  uint32_t wmax[2][4];   // largest S_v of each expand warp's keys
+  uint32_t there[4][4];  // which keys of a tile exist, by the ring of vec
+  int exponent[4];       // E of a tile, by the same ring
+
   int b, tile, head;  // this CTA's unit; b < 0: none
   uint32_t tmem_base;
   volatile int abort;
 };
 
-template <int D>
+template <int D, int G, bool kBf16>
 struct Cfg {
-  static constexpr int kQBytes = kM * D * 2;   // one Q tile
-  static constexpr int kKBytes = kN * D * 2;   // one K tile, one V^T tile
-  static constexpr int kVecFloats = 3 * kN;    // ks, lv, 1 / S_v
-  static constexpr int kSmem = 1024 + 2 * kQBytes + 4 * kKBytes + 4 * kVecFloats * 4 +
+  static constexpr bool kSplitK = G > 1;            // K = hi + lo
+  static constexpr bool kSplitV = G > 1 && !kBf16;  // V = hi + lo
+  static constexpr bool kScaleP = G == 1 && !kBf16; // S_v 2^-E meets p
+  static constexpr int kKBufs = kSplitK ? 1 : 2;
+  static constexpr int kVBufs = kSplitV ? 1 : 2;
+  static constexpr int kQBytes = kM * D * 2;  // one Q tile
+  static constexpr int kTBytes = kN * D * 2;  // one K tile, one V^T tile; hi and lo are two
+  static constexpr int kVecFloats = (kSplitK ? 0 : kN) + (kScaleP ? kN : 0);  // ks, S_v 2^-E
+  static constexpr int kSmem = 1024 + 2 * kQBytes + 4 * kTBytes + 4 * kVecFloats * 4 +
                                static_cast<int>(sizeof(Ctl));
 };
 
@@ -95,11 +112,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -123,6 +135,11 @@ __device__ __forceinline__ uint32_t bsub2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
 template <bool kBf16>
 __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
@@ -179,12 +196,14 @@ __device__ __forceinline__ int request_tiles(const Kv4AttnArgs& a, int b) {
   return rows > a.most_rows ? static_cast<int>((rows + kRowsCta - 1) / kRowsCta) : 0;
 }
 
-// One row's 128 scores: p = 2^(s + lv + up) as binary16 pairs, their sum over S_v, and the
-// largest exponent. kMask: only keys low < pos <= lim count.
-template <bool kMask>
-__device__ __forceinline__ float row_pass(uint32_t t_s, uint32_t vs, float up, int pos0, int lim,
-                                          int low, uint32_t (&p)[kN / 64][32], float2& sum) {
-  const float2 up2 = make_float2(up, up);
+// One row's 128 scores: p = 2^(s ks + up) as binary16 pairs (times the key's value scale where
+// kSv), their sum, and the largest exponent. ks from shared memory where kKs, else `k1`.
+// kMask: only keys low < pos <= lim count that `there` has.
+template <bool kKs, bool kSv, bool kMask>
+__device__ __forceinline__ float row_pass(uint32_t t_s, uint32_t vs, float k1, float up, int pos0,
+                                          int lim, int low, const uint32_t* there,
+                                          uint32_t (&p)[kN / 64][32], float2& sum) {
+  const float2 up2 = make_float2(up, up), k2 = make_float2(k1, k1);
   float mx = -INFINITY;
   sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -192,27 +211,37 @@ __device__ __forceinline__ float row_pass(uint32_t t_s, uint32_t vs, float up, i
     uint32_t v[32];
     tmem_ld32(t_s + 32 * c, v);
     tmem_wait_ld();
+    uint32_t bits = 0;
+    if (kMask) bits = there[c];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const float4 ks = lds_f4(vs + (32 * c + 4 * q) * 4);
-      const float4 lv = lds_f4(vs + (kN + 32 * c + 4 * q) * 4);
-      const float4 is = lds_f4(vs + (2 * kN + 32 * c + 4 * q) * 4);
+      float2 ka = k2, kb = k2;
+      if (kKs) {
+        const float4 ks = lds_f4(vs + (32 * c + 4 * q) * 4);
+        ka = make_float2(ks.x, ks.y);
+        kb = make_float2(ks.z, ks.w);
+      }
       float2 s0 = __ffma2_rn(make_float2(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1])),
-                             make_float2(ks.x, ks.y), __fadd2_rn(make_float2(lv.x, lv.y), up2));
+                             ka, up2);
       float2 s1 = __ffma2_rn(make_float2(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])),
-                             make_float2(ks.z, ks.w), __fadd2_rn(make_float2(lv.z, lv.w), up2));
+                             kb, up2);
       if (kMask) {
         const int pos = pos0 + 32 * c + 4 * q;
-        if (pos > lim || pos <= low) s0.x = -INFINITY;
-        if (pos + 1 > lim || pos + 1 <= low) s0.y = -INFINITY;
-        if (pos + 2 > lim || pos + 2 <= low) s1.x = -INFINITY;
-        if (pos + 3 > lim || pos + 3 <= low) s1.y = -INFINITY;
+        if (pos > lim || pos <= low || !((bits >> (4 * q)) & 1u)) s0.x = -INFINITY;
+        if (pos + 1 > lim || pos + 1 <= low || !((bits >> (4 * q + 1)) & 1u)) s0.y = -INFINITY;
+        if (pos + 2 > lim || pos + 2 <= low || !((bits >> (4 * q + 2)) & 1u)) s1.x = -INFINITY;
+        if (pos + 3 > lim || pos + 3 <= low || !((bits >> (4 * q + 3)) & 1u)) s1.y = -INFINITY;
       }
       mx = fmaxf(fmaxf(mx, fmaxf(s0.x, s0.y)), fmaxf(s1.x, s1.y));
-      const float2 p0 = make_float2(ex2(s0.x), ex2(s0.y));
-      const float2 p1 = make_float2(ex2(s1.x), ex2(s1.y));
-      sum = __ffma2_rn(p0, make_float2(is.x, is.y), sum);
-      sum = __ffma2_rn(p1, make_float2(is.z, is.w), sum);
+      float2 p0 = make_float2(ex2(s0.x), ex2(s0.y));
+      float2 p1 = make_float2(ex2(s1.x), ex2(s1.y));
+      sum = __fadd2_rn(p0, sum);
+      sum = __fadd2_rn(p1, sum);
+      if (kSv) {
+        const float4 sv = lds_f4(vs + (kN + 32 * c + 4 * q) * 4);
+        p0 = __fmul2_rn(p0, make_float2(sv.x, sv.y));
+        p1 = __fmul2_rn(p1, make_float2(sv.z, sv.w));
+      }
       p[c >> 1][16 * (c & 1) + 2 * q] = half2_bits(p0.x, p0.y);
       p[c >> 1][16 * (c & 1) + 2 * q + 1] = half2_bits(p1.x, p1.y);
     }
@@ -220,16 +249,16 @@ __device__ __forceinline__ float row_pass(uint32_t t_s, uint32_t vs, float up, i
   return mx;
 }
 
-template <int D, bool kBf16>
+template <int D, int G, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnArgs a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, G, kBf16>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = base;                      // [2][atom][128 rows][128 B]
-  uint8_t* sK = sQ + 2 * C::kQBytes;       // [2][atom][128 keys][128 B]
-  uint8_t* sV = sK + 2 * C::kKBytes;       // [2][2 atoms of 64 keys][D rows][128 B]
-  float* vec = reinterpret_cast<float*>(sV + 2 * C::kKBytes);  // [4][ks, lv, isv][128]
+  uint8_t* sK = sQ + 2 * C::kQBytes;       // [2: buffer, or hi and lo][atom][128 keys][128 B]
+  uint8_t* sV = sK + 2 * C::kTBytes;       // [2: as for K][2 atoms of 64 keys][D rows][128 B]
+  float* vec = reinterpret_cast<float*>(sV + 2 * C::kTBytes);  // [4][ks, S_v 2^-E][128]
   Ctl* ctl = reinterpret_cast<Ctl*>(vec + 4 * C::kVecFloats);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -279,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
         mbar_init(&ctl->p_full[i], 4);
       }
       for (int i = 0; i < 4; ++i) mbar_init(&ctl->vec_full[i], 4);
+      mbar_init(&ctl->w_full, 4);
       mbar_init(&ctl->o_full, 1);
       ctl->abort = 0;
       fence_barrier_init();
@@ -357,8 +387,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
     const uint32_t t_s = t_row + i * kN;
     const uint32_t t_o = t_row + 2 * kN + i * 128;
     const uint32_t vec_s = smem_u32(vec);
+    // K of fp16 with several scales is taken times 2^-4, so that no S_k (q - Z) overflows
+    const float k1 = a.scale_log2 * (kBf16 ? 1.0f : 16.0f);
     float m = -INFINITY, l = 0.0f;
+    int exponent = 0;
     bool ok = true;
+    auto rescale = [&](float f) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(t_o + 32 * c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+        tmem_st32(t_o + 32 * c, v);
+      }
+    };
     for (int j = 0; j < u.nt; ++j) {
       if (!wait_warp(&ctl->s_full[i], j & 1, ctl, a.status) ||
           !wait_warp(&ctl->vec_full[j & 3], (j >> 2) & 1, ctl, a.status)) {
@@ -367,16 +411,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
       }
       tc_fence_after();
       const uint32_t vs = vec_s + (j & 3) * C::kVecFloats * 4;
+      const uint32_t* there = ctl->there[j & 3];
       const int pos0 = (u.t0 + j) * kN;
-      const bool safe = pos0 + kN <= safe_end && pos0 >= safe_begin;
+      const bool safe = pos0 + kN <= safe_end && pos0 >= safe_begin &&
+                        (there[0] & there[1] & there[2] & there[3]) == 0xFFFFFFFFu;
+      const int e = ctl->exponent[j & 3];
+      if (e != exponent) {
+        if (j > 0) rescale(ex2(static_cast<float>(exponent - e)));
+        exponent = e;
+      }
       uint32_t p[kN / 64][32];
       float2 sum;
       // two passes settle any scores that fp32 can tell apart; the bound ends it for others
       for (int pass = 0; pass < 3; ++pass) {
         const float ref = m == -INFINITY ? 0.0f : m;
-        float mx = safe ? row_pass<false>(t_s, vs, kLift - ref, 0, 0, 0, p, sum)
-                        : row_pass<true>(t_s, vs, kLift - ref, pos0, lim,
-                                         a.window > 0 ? lim - a.window : -1, p, sum);
+        const float mx =
+            safe ? row_pass<!C::kSplitK, C::kScaleP, false>(t_s, vs, k1, kLift - ref, 0, 0, 0,
+                                                            there, p, sum)
+                 : row_pass<!C::kSplitK, C::kScaleP, true>(t_s, vs, k1, kLift - ref, pos0, lim,
+                                                           a.window > 0 ? lim - a.window : -1,
+                                                           there, p, sum);
         // mx is relative to m: above kLift + kHeadroom m has to move (from -inf: always)
         const bool over = m == -INFINITY ? mx > -INFINITY : mx > kLift + kHeadroom;
         if (!__any_sync(0xffffffffu, over)) break;
@@ -384,17 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
         const float f = to == -INFINITY || m == to ? 1.0f : ex2(m - to);
         m = to;
         l *= f;
-        if (j > 0) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            tmem_ld32(t_o + 32 * c, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-            tmem_st32(t_o + 32 * c, v);
-          }
-        }
+        if (j > 0) rescale(f);
       }
       l += sum.x + sum.y;
 #pragma unroll
@@ -407,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
     // --- the rows' results
     if (ok && wait_warp(&ctl->o_full, 0, ctl, a.status)) {
       tc_fence_after();
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv = l == 0.0f ? 0.0f : ex2(static_cast<float>(exponent)) / l;
       uint16_t* dst = a.out + static_cast<int64_t>(u.q0 + tok) * a.o_tok +
                       static_cast<int64_t>(h) * a.o_head;
 #pragma unroll
@@ -455,27 +499,47 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
       }
       return kc.data + (static_cast<int64_t>(blk) * kc.kv_heads + head) * kc.chunk_bytes();
     };
-    uint4 kw[D / 32];
-    uint32_t ksz, ksv;  // scale words of the thread's key, of K and V
+    uint32_t kw[4][D / 32];
+    uint32_t ksz[G], svmax;  // scale words of the thread's key; its largest S_v
     bool k_there;
     uint32_t vw[8][VB / 4];
-    uint32_t vsz[8];
+    uint32_t vsz[8][G];
     auto load_k = [&](int j) {
       const int64_t pos = static_cast<int64_t>(u.t0 + j) * kN + e;
       const uint8_t* ch = chunk_of(pos);
       k_there = ch != nullptr;
-      ksz = ksv = 0;
+      svmax = 0;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) kw[c] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < G; ++i) ksz[i] = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) kw[c][q] = 0;
       if (ch) {
         const int t = static_cast<int>(pos) & bmask;
-        // word c (D/32) + j of the row is word 4 j + c of its dimensions
-        const uint4* src = reinterpret_cast<const uint4*>(ch + t * (D / 2));
+        // word c (D/32) + q of the row is word 4 q + c of its dimensions
+        const uint8_t* src = ch + t * (D / 2);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) kw[c] = ld_nc_u4(src + c);
-        const uint32_t* sz = reinterpret_cast<const uint32_t*>(ch + 2 * codes);
-        ksz = __ldg(sz + t);
-        ksv = __ldg(sz + kc.block + t);
+        for (int c = 0; c < 4; ++c) {
+          if (D == 128) {
+            const uint4 x = ld_nc_u4(src + 16 * c);
+            kw[c][0] = x.x;
+            kw[c][1] = x.y;
+            kw[c][D / 32 - 2] = x.z;
+            kw[c][D / 32 - 1] = x.w;
+          } else {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(src + 8 * c));
+            kw[c][0] = x.x;
+            kw[c][1] = x.y;
+          }
+        }
+        const uint32_t* sz = reinterpret_cast<const uint32_t*>(ch + 2 * codes) + t * G;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          ksz[i] = __ldg(sz + i);
+          const uint32_t v = __ldg(sz + kc.block * G + i) & 0xFFFFu;
+          svmax = v > svmax ? v : svmax;  // binary16 patterns >= 0 compare as integers
+        }
       }
     };
     auto load_v = [&](int j) {
@@ -483,13 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
       const uint8_t* ch = chunk_of(pos);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        vsz[k] = 0;
+#pragma unroll
+        for (int i = 0; i < G; ++i) vsz[k][i] = 0;
 #pragma unroll
         for (int q = 0; q < VB / 4; ++q) vw[k][q] = 0;
       }
       if (ch) {
         const int t = static_cast<int>(pos) & bmask;
-        const uint32_t* sz = reinterpret_cast<const uint32_t*>(ch + 2 * codes) + kc.block;
+        const uint32_t* sz = reinterpret_cast<const uint32_t*>(ch + 2 * codes) + kc.block * G;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (pos + k < u.kv) {
@@ -502,80 +567,146 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
             } else {
               vw[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
             }
-            vsz[k] = __ldg(sz + t + k);
+#pragma unroll
+            for (int i = 0; i < G; ++i) vsz[k][i] = __ldg(sz + (t + k) * G + i);
           }
         }
       }
     };
     load_k(0);
     load_v(0);
+    // E: S_v 2^-E stays below 2 where it meets p (p <= 2^14), below 2^12 where it meets 15
+    constexpr int kTop = C::kScaleP ? 0 : 4, kMost = C::kScaleP ? 0 : 11;
+    int exponent = -64;  // of no value
     const uint32_t sK0 = smem_u32(sK), sV0 = smem_u32(sV), vec0 = smem_u32(vec);
     for (int j = 0; j < u.nt; ++j) {
-      const int buf = j & 1;
-      if (j >= 2 && !wait_warp(&ctl->k_empty[buf], ((j >> 1) - 1) & 1, ctl, a.status)) break;
+      const int kb = C::kKBufs == 2 ? j & 1 : 0, vb = C::kVBufs == 2 ? j & 1 : 0;
+      if (j >= C::kKBufs &&
+          !wait_warp(&ctl->k_empty[kb], (j / C::kKBufs - 1) & 1, ctl, a.status))
+        break;
+      // the tile's largest S_v, so E, before anything that uses it
       {
-        const uint32_t z = ksz >> 16;
-        const uint32_t z2 = z | z << 16;
-        // Z as a binary16 integer: to Z + 128 in bf16, Z + 1024 and -(Z + 64) in binary16
-        uint32_t zz, zh = 0;
-        if (kBf16) {
-          const float zf = f16_bits_to_f32(z) + 128.0f;
-          zz = pack_bf16x2(zf, zf);
-        } else {
-          zz = hfma2(z2, 0x3C003C00u, 0x64006400u);
-          zh = hfma2(z2, 0xBC00BC00u, 0xD400D400u);
+        const uint32_t x = __reduce_max_sync(0xffffffffu, svmax);
+        const uint32_t bits = __ballot_sync(0xffffffffu, k_there);
+        if (lane == 0) {
+          ctl->wmax[j & 1][warp - 8] = x;
+          ctl->there[j & 3][warp - 8] = bits;
         }
-        const uint32_t dst = sK0 + buf * C::kKBytes + e * 128;
+        if (lane == 0) mbar_arrive(&ctl->w_full);
+        if (!wait_warp(&ctl->w_full, j & 1, ctl, a.status)) break;
+        uint32_t y = 0;
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          // chunk n of the row: natural word n = 4 j + c, stored word c (D/32) + j
-          const int at = (n & 3) * (D / 32) + (n >> 2);
-          const uint4 q4 = kw[at >> 2];
-          const uint32_t w = (at & 3) == 0 ? q4.x : (at & 3) == 1 ? q4.y : (at & 3) == 2 ? q4.z : q4.w;
-          sts128(dst + (n >> 3) * (kN * 128) + (((n & 7) ^ (e & 7)) << 4), expand_k<kBf16>(w, zz, zh));
+        for (int q = 0; q < 4; ++q) y = max(y, ctl->wmax[j & 1][q]);
+        if (y != 0) {
+          const int top = static_cast<int>(__float_as_uint(f16_bits_to_f32(y)) >> 23) - 127;
+          if (top - exponent > kMost) exponent = top - kTop;
         }
-        const float sv = fmaxf(f16_bits_to_f32(ksv & 0xFFFFu), 5.9604644775390625e-8f);
+        if (e == 0) ctl->exponent[j & 3] = exponent < -60 ? 0 : exponent;
+      }
+      const float down = exponent < -60 ? 0.0f : ex2(static_cast<float>(-exponent));
+      {
+        uint32_t zz[G], zh[G], sh[G], sl[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          const uint32_t z = ksz[i] >> 16, z2 = z | z << 16;
+          const float s = f16_bits_to_f32(ksz[i] & 0xFFFFu);
+          // Z as a binary16 integer: to Z + 128 in bf16, Z + 1024 and -(Z + 64) in binary16
+          if (kBf16) {
+            const float zf = f16_bits_to_f32(z) + 128.0f;
+            zz[i] = pack_bf16x2(zf, zf);
+            sh[i] = pack_bf16x2(s, s);  // S = sh + sl, 8 bits and the other 3
+            const float rest = s - bf16_lo(sh[i]);
+            sl[i] = pack_bf16x2(rest, rest);
+          } else {
+            zz[i] = hfma2(z2, 0x3C003C00u, 0x64006400u);
+            zh[i] = hfma2(z2, 0xBC00BC00u, 0xD400D400u);
+            sh[i] = half2_bits(s * 0.0625f, s * 0.0625f);
+          }
+        }
+        const uint32_t dst = sK0 + kb * C::kTBytes + e * 128;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {  // chunk n of the row: dimensions 8 n .. 8 n + 7
+          const int gi = n * G / (D / 8);
+          const uint4 x = expand_k<kBf16>(kw[n & 3][n >> 2], zz[gi], zh[gi]);
+          const uint32_t at = dst + (n >> 3) * (kN * 128) + (((n & 7) ^ (e & 7)) << 4);
+          if (!C::kSplitK) {
+            sts128(at, x);
+          } else {
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (kBf16) {
+                hi[q] = bfma2(xs[q], sh[gi], 0x80008000u);
+                lo[q] = bfma2(xs[q], sl[gi], bfma2(xs[q], sh[gi], hi[q] ^ 0x80008000u));
+              } else {
+                hi[q] = hfma2(xs[q], sh[gi], 0x80008000u);
+                lo[q] = hfma2(xs[q], sh[gi], hi[q] ^ 0x80008000u);
+              }
+            }
+            sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            sts128(at + C::kTBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          }
+        }
         const uint32_t vs = vec0 + (j & 3) * C::kVecFloats * 4 + e * 4;
-        sts_f32(vs, k_there ? f16_bits_to_f32(ksz & 0xFFFFu) * a.scale_log2 : 0.0f);
-        sts_f32(vs + kN * 4, k_there ? lg2(sv) : -INFINITY);
-        sts_f32(vs + 2 * kN * 4, k_there ? __fdividef(1.0f, sv) : 0.0f);
+        if (!C::kSplitK) sts_f32(vs, f16_bits_to_f32(ksz[0] & 0xFFFFu) * a.scale_log2);
+        if (C::kScaleP) sts_f32(vs + kN * 4, f16_bits_to_f32(svmax) * down);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&ctl->k_full[buf]);
+          mbar_arrive(&ctl->k_full[kb]);
           mbar_arrive(&ctl->vec_full[j & 3]);
         }
       }
       if (j + 1 < u.nt) load_k(j + 1);
-      if (j >= 2 && !wait_warp(&ctl->v_empty[buf], ((j >> 1) - 1) & 1, ctl, a.status)) break;
+      if (j >= C::kVBufs &&
+          !wait_warp(&ctl->v_empty[vb], (j / C::kVBufs - 1) & 1, ctl, a.status))
+        break;
       {
-        uint32_t zz[4], zh[4];
+        uint32_t zz[G][4], zh[G][4], sv[G][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t z2 = __byte_perm(vsz[2 * k], vsz[2 * k + 1], 0x7632);
-          zz[k] = hfma2(z2, 0x3C003C00u, 0x64006400u);
-          zh[k] = hfma2(z2, 0xBC00BC00u, 0xD400D400u);
-        }
-        const uint32_t dst = sV0 + buf * C::kKBytes + (vo >> 3) * (D * 128);
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t z2 = __byte_perm(vsz[2 * k][i], vsz[2 * k + 1][i], 0x7632);
+            zz[i][k] = hfma2(z2, 0x3C003C00u, 0x64006400u);
+            zh[i][k] = hfma2(z2, 0xBC00BC00u, 0xD400D400u);
+            if (!C::kScaleP)
+              sv[i][k] = half2_bits(f16_bits_to_f32(vsz[2 * k][i] & 0xFFFFu) * down,
+                                    f16_bits_to_f32(vsz[2 * k + 1][i] & 0xFFFFu) * down);
+          }
+        const uint32_t dst = sV0 + vb * C::kTBytes + (vo >> 3) * (D * 128);
 #pragma unroll
         for (int n = 0; n < VB; ++n) {  // byte n: dimensions 16 n + 2 vg (low nibble), + 1
-          uint32_t lo[4], hi[4];
+          const int gi = n * G / VB;
+          const int d0 = 16 * n + 2 * vg;
+          uint32_t x[2][4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t y = __byte_perm(vw[2 * k][n >> 2], vw[2 * k + 1][n >> 2],
                                            static_cast<uint32_t>(n & 3) |
                                                (static_cast<uint32_t>(4 + (n & 3)) << 8));
-            lo[k] = hsub2(and_or(y, 0x000F000Fu, 0x64006400u), zz[k]);
-            hi[k] = hfma2(and_or(y, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh[k]);
+            x[0][k] = hsub2(and_or(y, 0x000F000Fu, 0x64006400u), zz[gi][k]);
+            x[1][k] = hfma2(and_or(y, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zh[gi][k]);
           }
-          const int d0 = 16 * n + 2 * vg;
-          sts128(dst + d0 * 128 + (((vo & 7) ^ (d0 & 7)) << 4), make_uint4(lo[0], lo[1], lo[2], lo[3]));
-          sts128(dst + (d0 + 1) * 128 + (((vo & 7) ^ ((d0 + 1) & 7)) << 4),
-                 make_uint4(hi[0], hi[1], hi[2], hi[3]));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t at = dst + (d0 + h) * 128 + (((vo & 7) ^ ((d0 + h) & 7)) << 4);
+            uint32_t hi[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              hi[k] = C::kScaleP ? x[h][k] : hfma2(x[h][k], sv[gi][k], 0x80008000u);
+            sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            if (C::kSplitV) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) hi[k] = hfma2(x[h][k], sv[gi][k], hi[k] ^ 0x80008000u);
+              sts128(at + C::kTBytes, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            }
+          }
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->v_full[buf]);
+        if (lane == 0) mbar_arrive(&ctl->v_full[vb]);
       }
       if (j + 1 < u.nt) load_v(j + 1);
     }
@@ -588,11 +719,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
     constexpr uint32_t kIdescO = (1u << 4) | ((D >> 3) << 17) | ((kM >> 4) << 24);
     auto scores = [&](int i, int buf) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t at = (k >> 2) * (128 * 128) + (k & 3) * 32;
-        tc_mma(tmem + i * kN, sw128_desc(sQ + i * C::kQBytes + at),
-               sw128_desc(sK + buf * C::kKBytes + at), kIdescS, k != 0);
-      }
+      for (int part = 0; part < (C::kSplitK ? 2 : 1); ++part)
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = (k >> 2) * (128 * 128) + (k & 3) * 32;
+          tc_mma(tmem + i * kN, sw128_desc(sQ + i * C::kQBytes + at),
+                 sw128_desc(sK + (buf + part) * C::kTBytes + at), kIdescS, (part | k) != 0);
+        }
       tc_commit(&ctl->s_full[i]);
     };
     bool ok = wait_lane(&ctl->q_full[0], 0, ctl, a.status) &&
@@ -605,24 +738,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
       tc_commit(&ctl->k_empty[0]);
     }
     for (int j = 0; j < u.nt && ok; ++j) {
-      const int buf = j & 1;
+      const int vb = C::kVBufs == 2 ? j & 1 : 0;
+      const int kb = C::kKBufs == 2 ? (j + 1) & 1 : 0;  // of the next keys
       const bool more = j + 1 < u.nt;
-      ok = wait_lane(&ctl->v_full[buf], (j >> 1) & 1, ctl, a.status);
+      ok = wait_lane(&ctl->v_full[vb], (j / C::kVBufs) & 1, ctl, a.status);
       for (int i = 0; i < 2 && ok; ++i) {
         ok = wait_lane(&ctl->p_full[i], j & 1, ctl, a.status);
-        if (ok && more && i == 0) ok = wait_lane(&ctl->k_full[buf ^ 1], ((j + 1) >> 1) & 1, ctl, a.status);
+        if (ok && more && i == 0)
+          ok = wait_lane(&ctl->k_full[kb], ((j + 1) / C::kKBufs) & 1, ctl, a.status);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < kN / 16; ++k)
-          tc_mma_tmem_a(tmem + 2 * kN + i * 128, tmem + i * kN + 8 * k,
-                        sw128_desc(sV + buf * C::kKBytes + (k >> 2) * (D * 128) + (k & 3) * 32),
-                        kIdescO, (j | k) != 0);
-        if (more) scores(i, buf ^ 1);
+        for (int part = 0; part < (C::kSplitV ? 2 : 1); ++part)
+#pragma unroll
+          for (int k = 0; k < kN / 16; ++k)
+            tc_mma_tmem_a(tmem + 2 * kN + i * 128, tmem + i * kN + 8 * k,
+                          sw128_desc(sV + (vb + part) * C::kTBytes + (k >> 2) * (D * 128) + (k & 3) * 32),
+                          kIdescO, (j | part | k) != 0);
+        if (more) scores(i, kb);
       }
       if (!ok) break;
-      tc_commit(&ctl->v_empty[buf]);
-      if (more) tc_commit(&ctl->k_empty[buf ^ 1]);
+      tc_commit(&ctl->v_empty[vb]);
+      if (more) tc_commit(&ctl->k_empty[kb]);
     }
     // all issued MMAs have completed once this arrives
     tc_commit(&ctl->o_full);
@@ -638,33 +775,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
   }
 }
 
-template <int D, bool kBf16>
+template <int D, int G, bool kBf16>
 cudaError_t launch_t(const Kv4AttnArgs& a, int64_t units, cudaStream_t st) {
-  auto kern = kv4_prompt_kernel<D, kBf16>;
+  using C = Cfg<D, G, kBf16>;
+  auto kern = kv4_prompt_kernel<D, G, kBf16>;
   static std::atomic<bool> attr[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!attr[dev & 63].load(std::memory_order_acquire)) {
-    e = set_smem_attrs(kern, Cfg<D>::kSmem);
+    e = set_smem_attrs(kern, C::kSmem);
     if (e != cudaSuccess) return e;
     attr[dev & 63].store(true, std::memory_order_release);
   }
-  kern<<<static_cast<unsigned>(units), kThreads, Cfg<D>::kSmem, st>>>(a);
+  kern<<<static_cast<unsigned>(units), kThreads, C::kSmem, st>>>(a);
   return cudaGetLastError();
 }
 
-}  // namespace
+template <int D, int G>
+cudaError_t launch_g(const Kv4AttnArgs& a, int64_t units, cudaStream_t st) {
+  return a.bf16 ? launch_t<D, G, true>(a, units, st) : launch_t<D, G, false>(a, units, st);
+}
 
-bool kv4_prompt_ok(const Kv4AttnArgs& a) { return a.cache.groups() == 1; }
+}  // namespace
 
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs& a, cudaStream_t st) {
   // an upper bound of the units: the lengths are on the device, CTAs without a unit return
   const int64_t units = (static_cast<int64_t>(a.tokens) * a.ratio / kRowsCta + a.requests) *
                         a.cache.kv_heads;
-  if (a.cache.dim == 128)
-    return a.bf16 ? launch_t<128, true>(a, units, st) : launch_t<128, false>(a, units, st);
-  return a.bf16 ? launch_t<64, true>(a, units, st) : launch_t<64, false>(a, units, st);
+  const int groups = a.cache.groups();
+  if (a.cache.dim == 128) {
+    if (groups == 1) return launch_g<128, 1>(a, units, st);
+    return groups == 2 ? launch_g<128, 2>(a, units, st) : launch_g<128, 4>(a, units, st);
+  }
+  return groups == 1 ? launch_g<64, 1>(a, units, st) : launch_g<64, 2>(a, units, st);
 }
 
 }  // namespace wq
