@@ -47,7 +47,7 @@ constexpr float kLift = 6.0f, kHeadroom = 8.0f;  // p <= 2^14
 
 // Registers of a thread after the split: the launch gives every warpgroup 128, and the four
 // shares add up to the same.
-constexpr int kRegsSoftmax = 184, kRegsExpand = 96, kRegsIssue = 48;
+constexpr int kRegsSoftmax = 176, kRegsExpand = 112, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue == 4 * 128, "register split");
 template <int N>
 __device__ __forceinline__ void reg_inc() {
@@ -64,10 +64,8 @@ struct Ctl {
   uint64_t v_full[2], v_empty[2];
   uint64_t vec_full[4];
   uint64_t s_full[2], p_full[2];
-  uint64_t w_full;  // the expand warps have written wmax
   uint64_t o_full;
   int64_t scan[16];
-  uint32_t wmax[2][4];   // largest S_v of each expand warp's keys
   uint32_t there[4][4];  // which keys of a tile exist, by the ring of vec
   int exponent[4];       // E of a tile, by the same ring
 
@@ -90,21 +88,16 @@ struct Cfg {
                                static_cast<int>(sizeof(Ctl));
 };
 
+// Waits suspend the warp: one that polls takes issue slots from the softmax warps beside it
+// (a step of 128 keys took 3.2 us with polling expand warps).
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* ctl,
                                           unsigned* status) {
-  const bool ok = __all_sync(0xffffffffu, mbar_wait_spin_bounded(bar, parity, kLimitNs) && !ctl->abort);
+  const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kLimitNs) && !ctl->abort);
   if (!ok && (threadIdx.x & 31) == 0) {
     set_status(status, kStTimeout);
     ctl->abort = 1;
   }
   return ok;
-}
-__device__ __forceinline__ bool wait_lane(uint64_t* bar, uint32_t parity, Ctl* ctl,
-                                          unsigned* status) {
-  if (mbar_wait_spin_bounded(bar, parity, kLimitNs) && !ctl->abort) return true;
-  set_status(status, kStTimeout);
-  ctl->abort = 1;
-  return false;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -260,7 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
   uint8_t* sV = sK + 2 * C::kTBytes;       // [2: as for K][2 atoms of 64 keys][D rows][128 B]
   float* vec = reinterpret_cast<float*>(sV + 2 * C::kTBytes);  // [4][ks, S_v 2^-E][128]
   Ctl* ctl = reinterpret_cast<Ctl*>(vec + 4 * C::kVecFloats);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (broadcast, so that the compiler knows the roles' branches, and the operands of the MMAs,
+  // to be the same for a whole warp)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   // --- which unit: the CTA's index in the line of all requests' (row tile, KV head) pairs
   {
@@ -308,7 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
         mbar_init(&ctl->p_full[i], 4);
       }
       for (int i = 0; i < 4; ++i) mbar_init(&ctl->vec_full[i], 4);
-      mbar_init(&ctl->w_full, 4);
       mbar_init(&ctl->o_full, 1);
       ctl->abort = 0;
       fence_barrier_init();
@@ -488,29 +482,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
     const int64_t codes = static_cast<int64_t>(kc.block) * (D / 2);
     const int32_t* table = a.tables + b * a.ld_tables;
     const int bmask = kc.block - 1;
-    // chunk of the block that holds a key, or nullptr where there is none
-    auto chunk_of = [&](int64_t pos) -> const uint8_t* {
-      if (pos >= u.kv) return nullptr;
+    // Block that holds a key, -1 where there is none. It is asked for a tile ahead of the codes,
+    // which are loaded a tile ahead of their use: neither latency shows.
+    auto block_of = [&](int64_t pos) -> int {
+      if (pos >= u.kv) return -1;
       const int64_t place = pos >> kc.block_log2;
-      const int blk = place < a.width ? table[place] : -1;
+      return place < a.width ? __ldg(table + place) : -2;
+    };
+    auto chunk_of = [&](int blk) -> const uint8_t* {
       if (blk < 0 || blk >= kc.num_blocks) {
-        set_status(a.status, kStRange);
+        if (blk != -1) set_status(a.status, kStRange);
         return nullptr;
       }
       return kc.data + (static_cast<int64_t>(blk) * kc.kv_heads + head) * kc.chunk_bytes();
     };
+    const int64_t pos_k = static_cast<int64_t>(u.t0) * kN + e;           // of tile 0
+    const int64_t pos_v = static_cast<int64_t>(u.t0) * kN + 8 * vo;
+    const int64_t pos_s = static_cast<int64_t>(u.t0) * kN + 4 * lane;    // four keys for E
+    int blk_k = block_of(pos_k), blk_v = block_of(pos_v), blk_s = block_of(pos_s);
     uint32_t kw[4][D / 32];
-    uint32_t ksz[G], svmax;  // scale words of the thread's key; its largest S_v
+    uint32_t ksz[G], ksv[G];  // scale words of the thread's key, of K and V
+    uint4 tsz[G];             // V's of the lane's four keys
+    int t_there;              // how many of the four there are
     bool k_there;
     uint32_t vw[8][VB / 4];
     uint32_t vsz[8][G];
     auto load_k = [&](int j) {
-      const int64_t pos = static_cast<int64_t>(u.t0 + j) * kN + e;
-      const uint8_t* ch = chunk_of(pos);
+      const int64_t pos = pos_k + static_cast<int64_t>(j) * kN;
+      const uint8_t* ch = chunk_of(blk_k);
+      const uint8_t* cs = chunk_of(blk_s);
+      blk_k = block_of(pos + kN);
+      blk_s = block_of(pos_s + static_cast<int64_t>(j + 1) * kN);
       k_there = ch != nullptr;
-      svmax = 0;
+      t_there = 0;
 #pragma unroll
-      for (int i = 0; i < G; ++i) ksz[i] = 0;
+      for (int i = 0; i < G; ++i) ksz[i] = ksv[i] = 0;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -537,14 +543,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
 #pragma unroll
         for (int i = 0; i < G; ++i) {
           ksz[i] = __ldg(sz + i);
-          const uint32_t v = __ldg(sz + kc.block * G + i) & 0xFFFFu;
-          svmax = v > svmax ? v : svmax;  // binary16 patterns >= 0 compare as integers
+          if (C::kScaleP) ksv[i] = __ldg(sz + kc.block * G + i);
         }
+      }
+      if (cs) {
+        const int64_t ps = pos_s + static_cast<int64_t>(j) * kN;
+        const uint32_t* sz = reinterpret_cast<const uint32_t*>(cs + 2 * codes) +
+                             (kc.block + (static_cast<int>(ps) & bmask)) * G;
+#pragma unroll
+        for (int i = 0; i < G; ++i) tsz[i] = ld_nc_u4(sz + 4 * i);
+        t_there = u.kv - ps < 4 ? static_cast<int>(u.kv - ps) : 4;
       }
     };
     auto load_v = [&](int j) {
-      const int64_t pos = static_cast<int64_t>(u.t0 + j) * kN + 8 * vo;
-      const uint8_t* ch = chunk_of(pos);
+      const int64_t pos = pos_v + static_cast<int64_t>(j) * kN;
+      const uint8_t* ch = chunk_of(blk_v);
+      blk_v = block_of(pos + kN);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
 #pragma unroll
@@ -586,17 +600,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
         break;
       // the tile's largest S_v, so E, before anything that uses it
       {
-        const uint32_t x = __reduce_max_sync(0xffffffffu, svmax);
-        const uint32_t bits = __ballot_sync(0xffffffffu, k_there);
-        if (lane == 0) {
-          ctl->wmax[j & 1][warp - 8] = x;
-          ctl->there[j & 3][warp - 8] = bits;
-        }
-        if (lane == 0) mbar_arrive(&ctl->w_full);
-        if (!wait_warp(&ctl->w_full, j & 1, ctl, a.status)) break;
-        uint32_t y = 0;
+        uint32_t y = 0;  // binary16 patterns >= 0 compare as integers
 #pragma unroll
-        for (int q = 0; q < 4; ++q) y = max(y, ctl->wmax[j & 1][q]);
+        for (int i = 0; i < G; ++i) {  // G words of each of four keys
+          const uint32_t w[4] = {tsz[i].x, tsz[i].y, tsz[i].z, tsz[i].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if ((4 * i + q) / G < t_there) y = max(y, w[q] & 0xFFFFu);
+        }
+        y = __reduce_max_sync(0xffffffffu, y);  // alike in the four warps
+        const uint32_t bits = __ballot_sync(0xffffffffu, k_there);
+        if (lane == 0) ctl->there[j & 3][warp - 8] = bits;
         if (y != 0) {
           const int top = static_cast<int>(__float_as_uint(f16_bits_to_f32(y)) >> 23) - 127;
           if (top - exponent > kMost) exponent = top - kTop;
@@ -650,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
         }
         const uint32_t vs = vec0 + (j & 3) * C::kVecFloats * 4 + e * 4;
         if (!C::kSplitK) sts_f32(vs, f16_bits_to_f32(ksz[0] & 0xFFFFu) * a.scale_log2);
-        if (C::kScaleP) sts_f32(vs + kN * 4, f16_bits_to_f32(svmax) * down);
+        if (C::kScaleP) sts_f32(vs + kN * 4, f16_bits_to_f32(ksv[0] & 0xFFFFu) * down);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -712,58 +726,74 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
     }
   } else {
     reg_dec<kRegsIssue>();
-    if (warp == 12 && lane == 0) {
-    // ---------------------------------------------------------------------- MMA issuer
-    constexpr uint32_t kFmt = kBf16 ? (1u << 7) | (1u << 10) : 0u;
-    constexpr uint32_t kIdescS = (1u << 4) | kFmt | ((kN >> 3) << 17) | ((kM >> 4) << 24);
-    constexpr uint32_t kIdescO = (1u << 4) | ((D >> 3) << 17) | ((kM >> 4) << 24);
-    auto scores = [&](int i, int buf) {
+    if (warp == 12) {
+      // -------------------------------------------------------------------- MMA issuer
+      constexpr uint32_t kFmt = kBf16 ? (1u << 7) | (1u << 10) : 0u;
+      constexpr uint32_t kIdescS = (1u << 4) | kFmt | ((kN >> 3) << 17) | ((kM >> 4) << 24);
+      constexpr uint32_t kIdescO = (1u << 4) | ((D >> 3) << 17) | ((kM >> 4) << 24);
+      const bool leader = elect_one();
+      const uint32_t q_lo = sw128_desc_lo(sQ), k_lo = sw128_desc_lo(sK), v_lo = sw128_desc_lo(sV);
+      auto scores = [&](int i, int buf) {
+        const uint32_t qd = q_lo + i * (C::kQBytes >> 4), kd = k_lo + buf * (C::kTBytes >> 4);
 #pragma unroll
-      for (int part = 0; part < (C::kSplitK ? 2 : 1); ++part)
+        for (int part = 0; part < (C::kSplitK ? 2 : 1); ++part)
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t at = (k >> 2) * (128 * 128) + (k & 3) * 32;
-          tc_mma(tmem + i * kN, sw128_desc(sQ + i * C::kQBytes + at),
-                 sw128_desc(sK + (buf + part) * C::kTBytes + at), kIdescS, (part | k) != 0);
-        }
-      tc_commit(&ctl->s_full[i]);
-    };
-    bool ok = wait_lane(&ctl->q_full[0], 0, ctl, a.status) &&
-              wait_lane(&ctl->q_full[1], 0, ctl, a.status) &&
-              wait_lane(&ctl->k_full[0], 0, ctl, a.status);
-    if (ok) {
-      tc_fence_after();
-      scores(0, 0);
-      scores(1, 0);
-      tc_commit(&ctl->k_empty[0]);
-    }
-    for (int j = 0; j < u.nt && ok; ++j) {
-      const int vb = C::kVBufs == 2 ? j & 1 : 0;
-      const int kb = C::kKBufs == 2 ? (j + 1) & 1 : 0;  // of the next keys
-      const bool more = j + 1 < u.nt;
-      ok = wait_lane(&ctl->v_full[vb], (j / C::kVBufs) & 1, ctl, a.status);
-      for (int i = 0; i < 2 && ok; ++i) {
-        ok = wait_lane(&ctl->p_full[i], j & 1, ctl, a.status);
-        if (ok && more && i == 0)
-          ok = wait_lane(&ctl->k_full[kb], ((j + 1) / C::kKBufs) & 1, ctl, a.status);
-        if (!ok) break;
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+            tc_mma_lo(tmem + i * kN, qd + at, kd + part * (C::kTBytes >> 4) + at, kIdescS,
+                      (part | k) != 0);
+          }
+        tc_commit(&ctl->s_full[i]);
+      };
+      bool ok = wait_warp(&ctl->q_full[0], 0, ctl, a.status) &&
+                wait_warp(&ctl->q_full[1], 0, ctl, a.status) &&
+                wait_warp(&ctl->k_full[0], 0, ctl, a.status);
+      if (ok) {
         tc_fence_after();
-#pragma unroll
-        for (int part = 0; part < (C::kSplitV ? 2 : 1); ++part)
-#pragma unroll
-          for (int k = 0; k < kN / 16; ++k)
-            tc_mma_tmem_a(tmem + 2 * kN + i * 128, tmem + i * kN + 8 * k,
-                          sw128_desc(sV + (vb + part) * C::kTBytes + (k >> 2) * (D * 128) + (k & 3) * 32),
-                          kIdescO, (j | part | k) != 0);
-        if (more) scores(i, kb);
+        if (leader) {
+          scores(0, 0);
+          scores(1, 0);
+          tc_commit(&ctl->k_empty[0]);
+        }
       }
-      if (!ok) break;
-      tc_commit(&ctl->v_empty[vb]);
-      if (more) tc_commit(&ctl->k_empty[kb]);
-    }
-    // all issued MMAs have completed once this arrives
-    tc_commit(&ctl->o_full);
-    if (!mbar_wait_bounded(&ctl->o_full, 0, kLimitNs)) set_status(a.status, kStTimeout);
+      for (int j = 0; j < u.nt && ok; ++j) {
+        const int vb = C::kVBufs == 2 ? j & 1 : 0;
+        const int kb = C::kKBufs == 2 ? (j + 1) & 1 : 0;  // of the next keys
+        const bool more = j + 1 < u.nt;
+        const uint32_t vd = v_lo + vb * (C::kTBytes >> 4);
+        ok = wait_warp(&ctl->v_full[vb], (j / C::kVBufs) & 1, ctl, a.status);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ok = ok && wait_warp(&ctl->p_full[i], j & 1, ctl, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int part = 0; part < (C::kSplitV ? 2 : 1); ++part)
+#pragma unroll
+              for (int k = 0; k < kN / 16; ++k)
+                tc_mma_tmem_a_lo(tmem + 2 * kN + i * 128, tmem + i * kN + 8 * k,
+                                 vd + ((part * C::kTBytes + (k >> 2) * (D * 128) + (k & 3) * 32) >> 4),
+                                 kIdescO, (part | k) != 0 ? 1u : j != 0);
+          }
+          if (more) {
+            if (i == 0) {
+              ok = wait_warp(&ctl->k_full[kb], ((j + 1) / C::kKBufs) & 1, ctl, a.status);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            if (leader) scores(i, kb);
+          }
+        }
+        if (!ok) break;
+        if (leader) {
+          tc_commit(&ctl->v_empty[vb]);
+          if (more) tc_commit(&ctl->k_empty[kb]);
+        }
+      }
+      // all issued MMAs have completed once this arrives
+      if (leader) tc_commit(&ctl->o_full);
+      if (!mbar_wait_bounded(&ctl->o_full, 0, kLimitNs)) set_status(a.status, kStTimeout);
     }
   }
   __syncwarp();
