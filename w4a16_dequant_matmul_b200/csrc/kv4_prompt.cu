@@ -19,11 +19,12 @@
 // a key only ks comes from shared memory for every score: the loads of three of them (scale,
 // logarithm and reciprocal of S_v) bounded an earlier form, 3.6 us a step of 128 keys.
 //
-// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (and Q's load, the output); 8-11 expand: codes
-// straight from global memory, one tile ahead in registers, into the two-deep rings of K
-// (rows = keys) and V^T (rows = dimensions, built from octets of keys) in the 128-byte
-// swizzle; 12 issues the MMAs (13-15 are idle and give their registers to the softmax). K and Q hold each eight dimensions in the order 0 4 1 5 2 6 3 7,
-// in which a word's codes come apart by shifts.
+// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (and Q's load, the output); 8-11 expand the codes
+// into the two-deep rings of K (rows = keys) and V^T (rows = dimensions, built from octets of
+// keys) in the 128-byte swizzle; 12 issues the MMAs; 13 copies the codes and scales of a tile
+// into shared memory (in registers, loaded a tile ahead, they were spilled and waited for:
+// 3000 of a step's 5700 cycles). K and Q hold each eight dimensions in the order
+// 0 4 1 5 2 6 3 7, in which a word's codes come apart by shifts.
 //
 // Half a tile of keys is the unit of the pipeline: S_i has two places in TMEM, so that the
 // softmax of one half runs while the products of the other do, and P_i takes the place of the
@@ -50,7 +51,7 @@ constexpr float kLift = 6.0f, kHeadroom = 8.0f;  // p <= 2^14
 
 // Registers of a thread after the split: the launch gives every warpgroup 128, and the four
 // shares add up to the same.
-constexpr int kRegsSoftmax = 184, kRegsExpand = 96, kRegsIssue = 48;
+constexpr int kRegsSoftmax = 176, kRegsExpand = 96, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue == 4 * 128, "register split");
 template <int N>
 __device__ __forceinline__ void reg_inc() {
@@ -66,6 +67,7 @@ struct Ctl {
   uint64_t k_full[2], k_empty[2];
   uint64_t v_full[2], v_empty[2];
   uint64_t vec_full[4];
+  uint64_t rk_full, rk_empty, rv_full, rv_empty;  // the raw tiles
   uint64_t s_full[2][2], p_full[2][2];  // [tile][half]: the softmax may be a half ahead
   uint64_t o_done[2];
   uint64_t o_full;
@@ -88,8 +90,11 @@ struct Cfg {
   static constexpr int kQBytes = kM * D * 2;  // one Q tile
   static constexpr int kTBytes = kN * D * 2;  // one K tile, one V^T tile; hi and lo are two
   static constexpr int kVecFloats = (kSplitK ? 0 : kN) + (kScaleP ? kN : 0);  // ks, S_v 2^-E
-  static constexpr int kSmem = 1024 + 2 * kQBytes + 4 * kTBytes + 4 * kVecFloats * 4 +
-                               static_cast<int>(sizeof(Ctl));
+  static constexpr int kRawK = kN * (D / 2 + 8 * G);  // K codes, K and V scale words of a tile
+  static constexpr int kRawV = kN * (D / 2 + 4 * G);  // V codes, V scale words
+  static constexpr int kSmem = 1024 + 2 * kQBytes + 4 * kTBytes + kRawK + kRawV +
+                               4 * kVecFloats * 4 + static_cast<int>(sizeof(Ctl));
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
 // Waits suspend the warp: one that polls takes issue slots from the softmax warps beside it
@@ -141,6 +146,16 @@ __device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
 template <bool kBf16>
 __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
   return kBf16 ? pack_bf16x2(lo, hi) : half2_bits(lo, hi);
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
 }
 __device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -260,7 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
   uint8_t* sQ = base;                      // [2][atom][128 rows][128 B]
   uint8_t* sK = sQ + 2 * C::kQBytes;       // [2: buffer, or hi and lo][atom][128 keys][128 B]
   uint8_t* sV = sK + 2 * C::kTBytes;       // [2: as for K][2 atoms of 64 keys][D rows][128 B]
-  float* vec = reinterpret_cast<float*>(sV + 2 * C::kTBytes);  // [4][ks, S_v 2^-E][128]
+  uint8_t* rawK = sV + 2 * C::kTBytes;     // [128 rows of K codes][K scale words][V's]
+  uint8_t* rawV = rawK + C::kRawK;         // [128 rows of V codes][V scale words]
+  float* vec = reinterpret_cast<float*>(rawV + C::kRawV);  // [4][ks, S_v 2^-E][128]
   Ctl* ctl = reinterpret_cast<Ctl*>(vec + 4 * C::kVecFloats);
   // (broadcast, so that the compiler knows the roles' branches, and the operands of the MMAs,
   // to be the same for a whole warp)
@@ -315,6 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
         mbar_init(&ctl->o_done[i], 1);
       }
       for (int i = 0; i < 4; ++i) mbar_init(&ctl->vec_full[i], 4);
+      mbar_init(&ctl->rk_full, 1);
+      mbar_init(&ctl->rk_empty, 4);
+      mbar_init(&ctl->rv_full, 1);
+      mbar_init(&ctl->rv_empty, 4);
       mbar_init(&ctl->o_full, 1);
       ctl->abort = 0;
       fence_barrier_init();
@@ -497,145 +518,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
   } else if (warp < 12) {
     reg_dec<kRegsExpand>();
     // ------------------------------------------------------------------------ expand
-    const Kv4Cache& kc = a.cache;
     const int e = threadIdx.x - 256;  // 0..127: the key of K that this thread expands
-    // V: an octet of keys, and the column group g whose bytes hold dimensions 16 i + 2 g, + 1;
+    // V: an octet of keys, and the column group vg whose bytes hold dimensions 16 n + 2 vg, + 1;
     // eight lanes that store together differ in row mod 8 or octet, so on banks
     constexpr int VB = D / 16;  // bytes of a column group
-    const int vg = (lane & 3) | ((lane >> 1) & 4) | 0;  // lane bits 0, 1, 3
-    const int vo = 4 * (warp - 8) + (((lane >> 2) & 1) | ((lane >> 3) & 2));  // lane bits 2, 4
-    const int64_t codes = static_cast<int64_t>(kc.block) * (D / 2);
-    const int32_t* table = a.tables + b * a.ld_tables;
-    const int bmask = kc.block - 1;
-    // Block that holds a key, -1 where there is none. It is asked for a tile ahead of the codes,
-    // which are loaded a tile ahead of their use: neither latency shows.
-    auto block_of = [&](int64_t pos) -> int {
-      if (pos >= u.kv) return -1;
-      const int64_t place = pos >> kc.block_log2;
-      return place < a.width ? __ldg(table + place) : -2;
-    };
-    auto chunk_of = [&](int blk) -> const uint8_t* {
-      if (blk < 0 || blk >= kc.num_blocks) {
-        if (blk != -1) set_status(a.status, kStRange);
-        return nullptr;
-      }
-      return kc.data + (static_cast<int64_t>(blk) * kc.kv_heads + head) * kc.chunk_bytes();
-    };
-    const int64_t pos_k = static_cast<int64_t>(u.t0) * kN + e;           // of tile 0
-    const int64_t pos_v = static_cast<int64_t>(u.t0) * kN + 8 * vo;
-    const int64_t pos_s = static_cast<int64_t>(u.t0) * kN + 4 * lane;    // four keys for E
-    int blk_k = block_of(pos_k), blk_v = block_of(pos_v), blk_s = block_of(pos_s);
-    uint32_t kw[4][D / 32];
-    uint32_t ksz[G], ksv[G];  // scale words of the thread's key, of K and V
-    uint4 tsz[G];             // V's of the lane's four keys
-    int t_there;              // how many of the four there are
-    bool k_there;
-    uint32_t vw[8][VB / 4];
-    uint32_t vsz[8][G];
-    auto load_k = [&](int j) {
-      const int64_t pos = pos_k + static_cast<int64_t>(j) * kN;
-      const uint8_t* ch = chunk_of(blk_k);
-      const uint8_t* cs = chunk_of(blk_s);
-      blk_k = block_of(pos + kN);
-      blk_s = block_of(pos_s + static_cast<int64_t>(j + 1) * kN);
-      k_there = ch != nullptr;
-      t_there = 0;
-#pragma unroll
-      for (int i = 0; i < G; ++i) ksz[i] = ksv[i] = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) kw[c][q] = 0;
-      if (ch) {
-        const int t = static_cast<int>(pos) & bmask;
-        // word c (D/32) + q of the row is word 4 q + c of its dimensions
-        const uint8_t* src = ch + t * (D / 2);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (D == 128) {
-            const uint4 x = ld_nc_u4(src + 16 * c);
-            kw[c][0] = x.x;
-            kw[c][1] = x.y;
-            kw[c][D / 32 - 2] = x.z;
-            kw[c][D / 32 - 1] = x.w;
-          } else {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(src + 8 * c));
-            kw[c][0] = x.x;
-            kw[c][1] = x.y;
-          }
-        }
-        const uint32_t* sz = reinterpret_cast<const uint32_t*>(ch + 2 * codes) + t * G;
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-          ksz[i] = __ldg(sz + i);
-          if (C::kScaleP) ksv[i] = __ldg(sz + kc.block * G + i);
-        }
-      }
-      if (cs) {
-        const int64_t ps = pos_s + static_cast<int64_t>(j) * kN;
-        const uint32_t* sz = reinterpret_cast<const uint32_t*>(cs + 2 * codes) +
-                             (kc.block + (static_cast<int>(ps) & bmask)) * G;
-#pragma unroll
-        for (int i = 0; i < G; ++i) tsz[i] = ld_nc_u4(sz + 4 * i);
-        t_there = u.kv - ps < 4 ? static_cast<int>(u.kv - ps) : 4;
-      }
-    };
-    auto load_v = [&](int j) {
-      const int64_t pos = pos_v + static_cast<int64_t>(j) * kN;
-      const uint8_t* ch = chunk_of(blk_v);
-      blk_v = block_of(pos + kN);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-#pragma unroll
-        for (int i = 0; i < G; ++i) vsz[k][i] = 0;
-#pragma unroll
-        for (int q = 0; q < VB / 4; ++q) vw[k][q] = 0;
-      }
-      if (ch) {
-        const int t = static_cast<int>(pos) & bmask;
-        const uint32_t* sz = reinterpret_cast<const uint32_t*>(ch + 2 * codes) + kc.block * G;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (pos + k < u.kv) {
-            const int flip = (D == 128 && (k & 2)) ? 32 : 0;
-            const uint8_t* src = ch + codes + (t + k) * (D / 2) + ((VB * vg) ^ flip);
-            if (VB == 8) {
-              const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-              vw[k][0] = x.x;
-              vw[k][VB / 4 - 1] = x.y;
-            } else {
-              vw[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-            }
-#pragma unroll
-            for (int i = 0; i < G; ++i) vsz[k][i] = __ldg(sz + (t + k) * G + i);
-          }
-        }
-      }
-    };
-    load_k(0);
-    load_v(0);
+    const int vg = (lane & 3) | ((lane >> 1) & 4);                              // lane bits 0, 1, 3
+    const int vo = 4 * (warp - 8) + (((lane >> 2) & 1) | ((lane >> 3) & 2));    // lane bits 2, 4
+    const uint32_t rk = smem_u32(rawK), rv = smem_u32(rawV);
+    const uint32_t rk_sz = rk + kN * (D / 2), rk_szv = rk_sz + kN * 4 * G, rv_sz = rv + kN * (D / 2);
+    const uint32_t sK0 = smem_u32(sK), sV0 = smem_u32(sV), vec0 = smem_u32(vec);
     // E: S_v 2^-E stays below 2 where it meets p (p <= 2^14), below 2^12 where it meets 15
     constexpr int kTop = C::kScaleP ? 0 : 4, kMost = C::kScaleP ? 0 : 11;
     int exponent = -64;  // of no value
-    const uint32_t sK0 = smem_u32(sK), sV0 = smem_u32(sV), vec0 = smem_u32(vec);
     for (int j = 0; j < u.nt; ++j) {
       const int kb = C::kKBufs == 2 ? j & 1 : 0, vb = C::kVBufs == 2 ? j & 1 : 0;
+      if (!wait_warp(&ctl->rk_full, j & 1, ctl, a.status)) break;
       if (j >= C::kKBufs &&
           !wait_warp(&ctl->k_empty[kb], (j / C::kKBufs - 1) & 1, ctl, a.status))
         break;
+      // what lies where no key is may be anything: its scales and zero-points count as 0
+      const uint32_t* there = ctl->there[j & 3];
+      const bool k_there = (there[warp - 8] >> lane) & 1u;
       // the tile's largest S_v, so E, before anything that uses it
       {
+        const uint32_t four = there[lane >> 3] >> (4 * (lane & 7));
         uint32_t y = 0;  // binary16 patterns >= 0 compare as integers
 #pragma unroll
-        for (int i = 0; i < G; ++i) {  // G words of each of four keys
-          const uint32_t w[4] = {tsz[i].x, tsz[i].y, tsz[i].z, tsz[i].w};
+        for (int i = 0; i < G; ++i) {  // G words of each of the lane's four keys
+          const uint4 x = lds128(rk_szv + 16 * (G * lane + i));
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if ((4 * i + q) / G < t_there) y = max(y, w[q] & 0xFFFFu);
+            if ((four >> ((4 * i + q) / G)) & 1u) y = max(y, w[q] & 0xFFFFu);
         }
         y = __reduce_max_sync(0xffffffffu, y);  // alike in the four warps
-        const uint32_t bits = __ballot_sync(0xffffffffu, k_there);
-        if (lane == 0) ctl->there[j & 3][warp - 8] = bits;
         if (y != 0) {
           const int top = static_cast<int>(__float_as_uint(f16_bits_to_f32(y)) >> 23) - 127;
           if (top - exponent > kMost) exponent = top - kTop;
@@ -645,10 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
       const float down = exponent < -60 ? 0.0f : ex2(static_cast<float>(-exponent));
       {
         uint32_t zz[G], zh[G], sh[G], sl[G];
+        float s0 = 0.0f;
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          const uint32_t z = ksz[i] >> 16, z2 = z | z << 16;
-          const float s = f16_bits_to_f32(ksz[i] & 0xFFFFu);
+          const uint32_t sz = k_there ? lds32(rk_sz + 4 * (G * e + i)) : 0u;
+          const uint32_t z = sz >> 16, z2 = z | z << 16;
+          const float s = f16_bits_to_f32(sz & 0xFFFFu);
+          if (i == 0) s0 = s;
           // Z as a binary16 integer: to Z + 128 in bf16, Z + 1024 and -(Z + 64) in binary16
           if (kBf16) {
             const float zf = f16_bits_to_f32(z) + 128.0f;
@@ -664,55 +583,93 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
         }
         const uint32_t dst = sK0 + kb * C::kTBytes + e * 128;
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {  // chunk n of the row: dimensions 8 n .. 8 n + 7
-          const int gi = n * G / (D / 8);
-          const uint4 x = expand_k<kBf16>(kw[n & 3][n >> 2], zz[gi], zh[gi]);
-          const uint32_t at = dst + (n >> 3) * (kN * 128) + (((n & 7) ^ (e & 7)) << 4);
-          if (!C::kSplitK) {
-            sts128(at, x);
+        for (int c = 0; c < 4; ++c) {
+          // stored words cc (D/32) + q of the row are words 4 q + cc of its dimensions; lanes
+          // begin with different cc, so that the rows (D/2 bytes apart) do not meet on banks
+          const int cc = (c + (e >> 1)) & 3;
+          uint32_t w[D / 32];
+          if (D == 128) {
+            const uint4 x = lds128(rk + e * (D / 2) + 16 * cc);
+            w[0] = x.x, w[1] = x.y, w[D / 32 - 2] = x.z, w[D / 32 - 1] = x.w;
           } else {
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-            uint32_t hi[4], lo[4];
+            const uint2 x = lds64(rk + e * (D / 2) + 8 * cc);
+            w[0] = x.x, w[1] = x.y;
+          }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (kBf16) {
-                hi[q] = bfma2(xs[q], sh[gi], 0x80008000u);
-                lo[q] = bfma2(xs[q], sl[gi], bfma2(xs[q], sh[gi], hi[q] ^ 0x80008000u));
-              } else {
-                hi[q] = hfma2(xs[q], sh[gi], 0x80008000u);
-                lo[q] = hfma2(xs[q], sh[gi], hi[q] ^ 0x80008000u);
+          for (int q = 0; q < D / 32; ++q) {
+            const int n = 4 * q + cc;  // chunk: dimensions 8 n .. 8 n + 7
+            constexpr int kPer = D / 32 / G > 0 ? D / 32 / G : 1;
+            const int gi = q / kPer;
+            const uint4 x = expand_k<kBf16>(w[q], zz[gi], zh[gi]);
+            const uint32_t at = dst + (n >> 3) * (kN * 128) + (((n & 7) ^ (e & 7)) << 4);
+            if (!C::kSplitK) {
+              sts128(at, x);
+            } else {
+              const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (kBf16) {
+                  hi[k] = bfma2(xs[k], sh[gi], 0x80008000u);
+                  lo[k] = bfma2(xs[k], sl[gi], bfma2(xs[k], sh[gi], hi[k] ^ 0x80008000u));
+                } else {
+                  hi[k] = hfma2(xs[k], sh[gi], 0x80008000u);
+                  lo[k] = hfma2(xs[k], sh[gi], hi[k] ^ 0x80008000u);
+                }
               }
+              sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+              sts128(at + C::kTBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
             }
-            sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-            sts128(at + C::kTBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
         }
         const uint32_t vs = vec0 + (j & 3) * C::kVecFloats * 4 + e * 4;
-        if (!C::kSplitK) sts_f32(vs, f16_bits_to_f32(ksz[0] & 0xFFFFu) * a.scale_log2);
-        if (C::kScaleP) sts_f32(vs + kN * 4, f16_bits_to_f32(ksv[0] & 0xFFFFu) * down);
+        if (!C::kSplitK) sts_f32(vs, s0 * a.scale_log2);
+        if (C::kScaleP) {
+          const uint32_t sv = k_there ? lds32(rk_szv + 4 * e) : 0u;
+          sts_f32(vs + kN * 4, f16_bits_to_f32(sv & 0xFFFFu) * down);
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&ctl->k_full[kb]);
           mbar_arrive(&ctl->vec_full[j & 3]);
+          mbar_arrive(&ctl->rk_empty);
         }
       }
-      if (j + 1 < u.nt) load_k(j + 1);
+      if (!wait_warp(&ctl->rv_full, j & 1, ctl, a.status)) break;
       if (j >= C::kVBufs &&
           !wait_warp(&ctl->v_empty[vb], (j / C::kVBufs - 1) & 1, ctl, a.status))
         break;
       {
+        uint32_t vw[8][VB / 4];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int flip = (D == 128 && (k & 2)) ? 32 : 0;
+          const uint32_t at = rv + (8 * vo + k) * (D / 2) + ((VB * vg) ^ flip);
+          if (VB == 8) {
+            const uint2 x = lds64(at);
+            vw[k][0] = x.x;
+            vw[k][VB / 4 - 1] = x.y;
+          } else {
+            vw[k][0] = lds32(at);
+          }
+        }
+        const uint32_t eight = there[vo >> 2] >> (8 * (vo & 3));
         uint32_t zz[G][4], zh[G][4], sv[G][4];
 #pragma unroll
         for (int i = 0; i < G; ++i)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t z2 = __byte_perm(vsz[2 * k][i], vsz[2 * k + 1][i], 0x7632);
+            uint32_t w0 = lds32(rv_sz + 4 * (G * (8 * vo + 2 * k) + i));
+            uint32_t w1 = lds32(rv_sz + 4 * (G * (8 * vo + 2 * k + 1) + i));
+            if (!((eight >> (2 * k)) & 1u)) w0 = 0;
+            if (!((eight >> (2 * k + 1)) & 1u)) w1 = 0;
+            const uint32_t z2 = __byte_perm(w0, w1, 0x7632);
             zz[i][k] = hfma2(z2, 0x3C003C00u, 0x64006400u);
             zh[i][k] = hfma2(z2, 0xBC00BC00u, 0xD400D400u);
             if (!C::kScaleP)
-              sv[i][k] = half2_bits(f16_bits_to_f32(vsz[2 * k][i] & 0xFFFFu) * down,
-                                    f16_bits_to_f32(vsz[2 * k + 1][i] & 0xFFFFu) * down);
+              sv[i][k] = half2_bits(f16_bits_to_f32(w0 & 0xFFFFu) * down,
+                                    f16_bits_to_f32(w1 & 0xFFFFu) * down);
           }
         const uint32_t dst = sV0 + vb * C::kTBytes + (vo >> 3) * (D * 128);
 #pragma unroll
@@ -745,9 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->v_full[vb]);
+        if (lane == 0) {
+          mbar_arrive(&ctl->v_full[vb]);
+          mbar_arrive(&ctl->rv_empty);
+        }
       }
-      if (j + 1 < u.nt) load_v(j + 1);
     }
   } else {
     reg_dec<kRegsIssue>();
@@ -824,6 +783,78 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
       // all issued MMAs have completed once this arrives
       if (leader) tc_commit(&ctl->o_full);
       if (!mbar_wait_bounded(&ctl->o_full, 0, kLimitNs)) set_status(a.status, kStTimeout);
+    } else if (warp == 13) {
+      // ---------------------------------------------------------------------- producer
+      // Bulk copies of a tile's pieces (of blocks, or of 128 keys of longer ones): lane p takes
+      // piece p, for K as soon as the expand warps have read the last tile's, then for V.
+      const Kv4Cache& kc = a.cache;
+      const int plog = kc.block_log2 < 7 ? kc.block_log2 : 7;
+      const int piece = 1 << plog, pieces = kN >> plog;
+      const int64_t codes = static_cast<int64_t>(kc.block) * (D / 2);
+      const int32_t* table = a.tables + b * a.ld_tables;
+      auto block_of = [&](int j) -> int {  // -1: no keys, -2: keys that the table does not reach
+        const int64_t pos = static_cast<int64_t>(u.t0 + j) * kN + lane * piece;
+        if (lane >= pieces || pos >= u.kv) return -1;
+        const int64_t place = pos >> kc.block_log2;
+        return place < a.width ? __ldg(table + place) : -2;
+      };
+      int next = block_of(0), j = 0;
+      bool ok = true;
+      for (; j < u.nt; ++j) {
+        const int blk = next;
+        if (j + 1 < u.nt) next = block_of(j + 1);
+        const bool good = blk >= 0 && blk < kc.num_blocks;
+        if (!good && blk != -1) set_status(a.status, kStRange);
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, good));
+        const int64_t pos = static_cast<int64_t>(u.t0 + j) * kN + lane * piece;
+        const int at = static_cast<int>(pos & (kc.block - 1));
+        const uint8_t* src =
+            kc.data + (static_cast<int64_t>(good ? blk : 0) * kc.kv_heads + head) * kc.chunk_bytes();
+        const uint8_t* szk = src + 2 * codes + at * 4 * G;
+        const uint8_t* szv = szk + kc.block * 4 * G;
+        if (j > 0 && !wait_warp(&ctl->rk_empty, (j - 1) & 1, ctl, a.status)) {
+          ok = false;
+          break;
+        }
+        {  // the keys that exist, 32 a word: lanes 0 .. 3
+          const uint32_t ok_pieces = __ballot_sync(0xffffffffu, good);
+          if (lane < 4) {
+            uint32_t bits = 0;
+            for (int q = 0; q < 32; ++q) {
+              const int key = 32 * lane + q;
+              if (((ok_pieces >> (key >> plog)) & 1u) &&
+                  static_cast<int64_t>(u.t0 + j) * kN + key < u.kv)
+                bits |= 1u << q;
+            }
+            ctl->there[j & 3][lane] = bits;
+          }
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&ctl->rk_full, n * piece * (D / 2 + 8 * G));
+        __syncwarp();
+        if (good) {
+          bulk_g2s(rawK + lane * piece * (D / 2), src + at * (D / 2), piece * (D / 2), &ctl->rk_full);
+          bulk_g2s(rawK + kN * (D / 2) + lane * piece * 4 * G, szk, piece * 4 * G, &ctl->rk_full);
+          bulk_g2s(rawK + kN * (D / 2 + 4 * G) + lane * piece * 4 * G, szv, piece * 4 * G,
+                   &ctl->rk_full);
+        }
+        if (j > 0 && !wait_warp(&ctl->rv_empty, (j - 1) & 1, ctl, a.status)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&ctl->rv_full, n * piece * (D / 2 + 4 * G));
+        __syncwarp();
+        if (good) {
+          bulk_g2s(rawV + lane * piece * (D / 2), src + codes + at * (D / 2), piece * (D / 2),
+                   &ctl->rv_full);
+          bulk_g2s(rawV + kN * (D / 2) + lane * piece * 4 * G, szv, piece * 4 * G, &ctl->rv_full);
+        }
+      }
+      // never leave with copies in flight: the last tile that each buffer was asked for
+      const int last_k = ok ? u.nt - 1 : j, last_v = ok ? u.nt - 1 : j - 1;
+      if (!mbar_wait_bounded(&ctl->rk_full, last_k & 1, kLimitNs) ||
+          (last_v >= 0 && !mbar_wait_bounded(&ctl->rv_full, last_v & 1, kLimitNs)))
+        set_status(a.status, kStTimeout);
     }
   }
   __syncwarp();
