@@ -26,11 +26,9 @@
 // 3000 of a step's 5700 cycles). K and Q hold each eight dimensions in the order
 // 0 4 1 5 2 6 3 7, in which a word's codes come apart by shifts.
 //
-// Half a tile of keys is the unit of the pipeline: S_i has two places in TMEM, so that the
-// softmax of one half runs while the products of the other do, and P_i takes the place of the
-// scores it came from; the scores two halves on are issued behind the product that reads it.
-// (With whole tiles, where softmax and products of a row tile take turns, a step of 128 keys
-// took 2.7 us instead.)
+// S_i and P_i share TMEM: S_i of the next keys is issued behind the product that reads P_i.
+// When the softmax of tile i wakes for S_i, that product has completed too (the same commit),
+// so it may touch O_i.
 #include <atomic>
 
 #include "common.cuh"
@@ -43,7 +41,6 @@ namespace {
 
 constexpr int kM = 128;       // rows of a Q tile
 constexpr int kN = 128;       // keys of a tile
-constexpr int kH = kN / 2;    // keys of a score product, half a tile
 constexpr int kRowsCta = 2 * kM;
 constexpr int kThreads = 512;
 constexpr uint64_t kLimitNs = 2000000000ull;
@@ -68,8 +65,7 @@ struct Ctl {
   uint64_t v_full[2], v_empty[2];
   uint64_t vec_full[4];
   uint64_t rk_full, rk_empty, rv_full, rv_empty;  // the raw tiles
-  uint64_t s_full[2][2], p_full[2][2];  // [tile][half]: the softmax may be a half ahead
-  uint64_t o_done[2];
+  uint64_t s_full[2], p_full[2];
   uint64_t o_full;
   int64_t scan[16];
   uint32_t there[4][4];  // which keys of a tile exist, by the ring of vec
@@ -147,6 +143,13 @@ template <bool kBf16>
 __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
   return kBf16 ? pack_bf16x2(lo, hi) : half2_bits(lo, hi);
 }
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -184,7 +187,7 @@ __device__ __forceinline__ uint4 expand_k(uint32_t w, uint32_t zz, uint32_t zh) 
 struct Unit {
   int q0, rows, kv, row0;  // request's first row of Q, its rows and keys, the CTA's first row
   int shift;               // keys before the first query: row i sees keys up to shift + i / ratio
-  int t0, nt, nh;          // first tile of 128 keys, number of tiles, of half tiles
+  int t0, nt;              // first tile of 128 keys, number of tiles
 };
 
 __device__ __forceinline__ void request_rows(const Kv4AttnArgs& a, int b, int& q0, int& qn) {
@@ -201,30 +204,35 @@ __device__ __forceinline__ int request_tiles(const Kv4AttnArgs& a, int b) {
   return rows > a.most_rows ? static_cast<int>((rows + kRowsCta - 1) / kRowsCta) : 0;
 }
 
-// 64 scores of a row become exponents s ks + up, -inf where the key does not count (kMask: only
-// keys low < pos <= lim do that `bits` has). ks from shared memory where kKs, else `k1`.
-// Returns the largest.
-template <bool kKs, bool kMask>
-__device__ __forceinline__ float exponents(uint32_t (&v)[2][32], const float4* ks_at, float k1,
-                                           float up, int pos0, int lim, int low,
-                                           const uint32_t* there) {
+// One row's 128 scores: p = 2^(s ks + up) as binary16 pairs (times the key's value scale where
+// kSv), their sum, and the largest exponent. ks from shared memory where kKs, else `k1`.
+// kMask: only keys low < pos <= lim count that `there` has.
+template <bool kKs, bool kSv, bool kMask>
+__device__ __forceinline__ float row_pass(uint32_t t_s, uint32_t vs, float k1, float up, int pos0,
+                                          int lim, int low, const uint32_t* there,
+                                          uint32_t (&p)[kN / 64][32], float2& sum) {
   const float2 up2 = make_float2(up, up), k2 = make_float2(k1, k1);
-  float mx[2] = {-INFINITY, -INFINITY};
+  float mx = -INFINITY;
+  sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
+  for (int c = 0; c < kN / 32; ++c) {
+    uint32_t v[32];
+    tmem_ld32(t_s + 32 * c, v);
+    tmem_wait_ld();
     uint32_t bits = 0;
     if (kMask) bits = there[c];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      uint32_t* w = &v[c][4 * q];
       float2 ka = k2, kb = k2;
       if (kKs) {
-        const float4 ks = ks_at[8 * c + q];
+        const float4 ks = lds_f4(vs + (32 * c + 4 * q) * 4);
         ka = make_float2(ks.x, ks.y);
         kb = make_float2(ks.z, ks.w);
       }
-      float2 s0 = __ffma2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), ka, up2);
-      float2 s1 = __ffma2_rn(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), kb, up2);
+      float2 s0 = __ffma2_rn(make_float2(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1])),
+                             ka, up2);
+      float2 s1 = __ffma2_rn(make_float2(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])),
+                             kb, up2);
       if (kMask) {
         const int pos = pos0 + 32 * c + 4 * q;
         if (pos > lim || pos <= low || !((bits >> (4 * q)) & 1u)) s0.x = -INFINITY;
@@ -232,38 +240,21 @@ __device__ __forceinline__ float exponents(uint32_t (&v)[2][32], const float4* k
         if (pos + 2 > lim || pos + 2 <= low || !((bits >> (4 * q + 2)) & 1u)) s1.x = -INFINITY;
         if (pos + 3 > lim || pos + 3 <= low || !((bits >> (4 * q + 3)) & 1u)) s1.y = -INFINITY;
       }
-      mx[q & 1] = fmaxf(mx[q & 1], fmaxf(fmaxf(s0.x, s0.y), fmaxf(s1.x, s1.y)));
-      w[0] = __float_as_uint(s0.x);
-      w[1] = __float_as_uint(s0.y);
-      w[2] = __float_as_uint(s1.x);
-      w[3] = __float_as_uint(s1.y);
+      mx = fmaxf(fmaxf(mx, fmaxf(s0.x, s0.y)), fmaxf(s1.x, s1.y));
+      float2 p0 = make_float2(ex2(s0.x), ex2(s0.y));
+      float2 p1 = make_float2(ex2(s1.x), ex2(s1.y));
+      sum = __fadd2_rn(p0, sum);
+      sum = __fadd2_rn(p1, sum);
+      if (kSv) {
+        const float4 sv = lds_f4(vs + (kN + 32 * c + 4 * q) * 4);
+        p0 = __fmul2_rn(p0, make_float2(sv.x, sv.y));
+        p1 = __fmul2_rn(p1, make_float2(sv.z, sv.w));
+      }
+      p[c >> 1][16 * (c & 1) + 2 * q] = half2_bits(p0.x, p0.y);
+      p[c >> 1][16 * (c & 1) + 2 * q + 1] = half2_bits(p1.x, p1.y);
     }
   }
-  return fmaxf(mx[0], mx[1]);
-}
-
-// Their powers p as binary16 pairs (times the key's value scale where kSv), and their sum.
-template <bool kSv>
-__device__ __forceinline__ float powers(const uint32_t (&v)[2][32], const float4* sv_at,
-                                        uint32_t (&p)[32]) {
-  float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const uint32_t* w = &v[q >> 3][4 * (q & 7)];
-    float2 p0 = make_float2(ex2(__uint_as_float(w[0])), ex2(__uint_as_float(w[1])));
-    float2 p1 = make_float2(ex2(__uint_as_float(w[2])), ex2(__uint_as_float(w[3])));
-    sum[0] = __fadd2_rn(p0, sum[0]);
-    sum[1] = __fadd2_rn(p1, sum[1]);
-    if (kSv) {
-      const float4 sv = sv_at[q];
-      p0 = __fmul2_rn(p0, make_float2(sv.x, sv.y));
-      p1 = __fmul2_rn(p1, make_float2(sv.z, sv.w));
-    }
-    p[2 * q] = half2_bits(p0.x, p0.y);
-    p[2 * q + 1] = half2_bits(p1.x, p1.y);
-  }
-  sum[0] = __fadd2_rn(sum[0], sum[1]);
-  return sum[0].x + sum[0].y;
+  return mx;
 }
 
 template <int D, int G, bool kBf16>
@@ -325,11 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
         mbar_init(&ctl->k_empty[i], 1);
         mbar_init(&ctl->v_full[i], 4);
         mbar_init(&ctl->v_empty[i], 1);
-        mbar_init(&ctl->s_full[i][0], 1);
-        mbar_init(&ctl->s_full[i][1], 1);
-        mbar_init(&ctl->p_full[i][0], 4);
-        mbar_init(&ctl->p_full[i][1], 4);
-        mbar_init(&ctl->o_done[i], 1);
+        mbar_init(&ctl->s_full[i], 1);
+        mbar_init(&ctl->p_full[i], 4);
       }
       for (int i = 0; i < 4; ++i) mbar_init(&ctl->vec_full[i], 4);
       mbar_init(&ctl->rk_full, 1);
@@ -374,9 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
       first = (a.causal ? static_cast<int64_t>(u.shift) + u.row0 / a.ratio : u.kv - 1) - a.window + 1;
     if (first < 0) first = 0;
     u.t0 = static_cast<int>(first / kN);
-    const int64_t left = end - static_cast<int64_t>(u.t0) * kN;
-    u.nh = left > 0 ? static_cast<int>((left + kH - 1) / kH) : 1;
-    u.nt = (u.nh + 1) >> 1;
+    const int64_t last_tile = (end + kN - 1) / kN;
+    u.nt = last_tile > u.t0 ? static_cast<int>(last_tile - u.t0) : 1;
   }
 
   if (warp < 8) {
@@ -414,79 +401,67 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
     const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t t_s = t_row + i * kN;
     const uint32_t t_o = t_row + 2 * kN + i * 128;
+    const uint32_t vec_s = smem_u32(vec);
     // K of fp16 with several scales is taken times 2^-4, so that no S_k (q - Z) overflows
     const float k1 = a.scale_log2 * (kBf16 ? 1.0f : 16.0f);
     float m = -INFINITY, l = 0.0f;
     int exponent = 0;
     bool ok = true;
-    for (int h = 0; h < u.nh; ++h) {
-      const int j = h >> 1, half = h & 1;
-      if (!wait_warp(&ctl->s_full[i][half], j & 1, ctl, a.status) ||
+    auto rescale = [&](float f) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(t_o + 32 * c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+        tmem_st32(t_o + 32 * c, v);
+      }
+    };
+    for (int j = 0; j < u.nt; ++j) {
+      if (!wait_warp(&ctl->s_full[i], j & 1, ctl, a.status) ||
           !wait_warp(&ctl->vec_full[j & 3], (j >> 2) & 1, ctl, a.status)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint32_t v[2][32];
-      tmem_ld32(t_s + kH * half, v[0]);
-      tmem_ld32(t_s + kH * half + 32, v[1]);
-      const float4* vs = reinterpret_cast<const float4*>(vec + (j & 3) * C::kVecFloats + kH * half);
-      const uint32_t* there = &ctl->there[j & 3][2 * half];
-      const int pos0 = (u.t0 + j) * kN + kH * half;
-      const bool safe = pos0 + kH <= safe_end && pos0 >= safe_begin &&
-                        (there[0] & there[1]) == 0xFFFFFFFFu;
+      const uint32_t vs = vec_s + (j & 3) * C::kVecFloats * 4;
+      const uint32_t* there = ctl->there[j & 3];
+      const int pos0 = (u.t0 + j) * kN;
+      const bool safe = pos0 + kN <= safe_end && pos0 >= safe_begin &&
+                        (there[0] & there[1] & there[2] & there[3]) == 0xFFFFFFFFu;
       const int e = ctl->exponent[j & 3];
-      float f = 1.0f;  // what O is still to be multiplied by
       if (e != exponent) {
-        f = ex2(static_cast<float>(exponent - e));
+        if (j > 0) rescale(ex2(static_cast<float>(exponent - e)));
         exponent = e;
       }
-      const float ref = m == -INFINITY ? 0.0f : m;
-      tmem_wait_ld();
-      const float mx =
-          safe ? exponents<!C::kSplitK, false>(v, vs, k1, kLift - ref, 0, 0, 0, there)
-               : exponents<!C::kSplitK, true>(v, vs, k1, kLift - ref, pos0, lim,
-                                              a.window > 0 ? lim - a.window : -1, there);
-      uint32_t p[32];
-      float sum = powers<C::kScaleP>(v, vs + kN / 4, p);
-      // mx is relative to m: above kLift + kHeadroom (from -inf: always) m moves, with all that
-      // was counted by it, and these powers are taken again
-      const bool over = m == -INFINITY ? mx > -INFINITY : mx > kLift + kHeadroom;
-      if (__any_sync(0xffffffffu, over || f != 1.0f)) {
+      uint32_t p[kN / 64][32];
+      float2 sum;
+      // two passes settle any scores that fp32 can tell apart; the bound ends it for others
+      for (int pass = 0; pass < 3; ++pass) {
+        const float ref = m == -INFINITY ? 0.0f : m;
+        const float mx =
+            safe ? row_pass<!C::kSplitK, C::kScaleP, false>(t_s, vs, k1, kLift - ref, 0, 0, 0,
+                                                            there, p, sum)
+                 : row_pass<!C::kSplitK, C::kScaleP, true>(t_s, vs, k1, kLift - ref, pos0, lim,
+                                                           a.window > 0 ? lim - a.window : -1,
+                                                           there, p, sum);
+        // mx is relative to m: above kLift + kHeadroom m has to move (from -inf: always)
+        const bool over = m == -INFINITY ? mx > -INFINITY : mx > kLift + kHeadroom;
+        if (!__any_sync(0xffffffffu, over)) break;
         const float to = fmaxf(m, ref + (mx - kLift));
-        const float g = to == -INFINITY || m == to ? 1.0f : ex2(m - to);
-        const float back = to == -INFINITY ? 0.0f : ref - to;
+        const float f = to == -INFINITY || m == to ? 1.0f : ex2(m - to);
         m = to;
-        l *= g;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int q = 0; q < 32; ++q) v[c][q] = __float_as_uint(__uint_as_float(v[c][q]) + back);
-        sum = powers<C::kScaleP>(v, vs + kN / 4, p);
-        if (h > 0) {
-          if (!wait_warp(&ctl->o_done[i], (h - 1) & 1, ctl, a.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          f *= g;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            tmem_ld32(t_o + 32 * c, v[0]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int q = 0; q < 32; ++q)
-              v[0][q] = __float_as_uint(__uint_as_float(v[0][q]) * f);
-            tmem_st32(t_o + 32 * c, v[0]);
-          }
-        }
+        l *= f;
+        if (j > 0) rescale(f);
       }
-      l += sum;
-      tmem_st32(t_s + kH * half, p);
+      l += sum.x + sum.y;
+#pragma unroll
+      for (int c = 0; c < kN / 64; ++c) tmem_st32(t_s + 32 * c, p[c]);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->p_full[i][half]);
+      if (lane == 0) mbar_arrive(&ctl->p_full[i]);
     }
     // --- the rows' results
     if (ok && wait_warp(&ctl->o_full, 0, ctl, a.status)) {
@@ -582,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
           }
         }
         const uint32_t dst = sK0 + kb * C::kTBytes + e * 128;
-#pragma unroll
+#pragma unroll 1  // (the roles' code shares the instruction cache: 643 us unrolled, 614 so)
         for (int c = 0; c < 4; ++c) {
           // stored words cc (D/32) + q of the row are words 4 q + cc of its dimensions; lanes
           // begin with different cc, so that the rows (D/2 bytes apart) do not meet on banks
@@ -713,24 +688,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
     if (warp == 12) {
       // -------------------------------------------------------------------- MMA issuer
       constexpr uint32_t kFmt = kBf16 ? (1u << 7) | (1u << 10) : 0u;
-      constexpr uint32_t kIdescS = (1u << 4) | kFmt | ((kH >> 3) << 17) | ((kM >> 4) << 24);
+      constexpr uint32_t kIdescS = (1u << 4) | kFmt | ((kN >> 3) << 17) | ((kM >> 4) << 24);
       constexpr uint32_t kIdescO = (1u << 4) | ((D >> 3) << 17) | ((kM >> 4) << 24);
       const bool leader = elect_one();
       const uint32_t q_lo = sw128_desc_lo(sQ), k_lo = sw128_desc_lo(sK), v_lo = sw128_desc_lo(sV);
-      auto scores = [&](int i, int h) {
-        const int buf = C::kKBufs == 2 ? (h >> 1) & 1 : 0, half = h & 1;
-        const uint32_t qd = q_lo + i * (C::kQBytes >> 4);
-        const uint32_t kd = k_lo + ((buf * C::kTBytes + half * (kH * 128)) >> 4);
+      auto scores = [&](int i, int buf) {
+        const uint32_t qd = q_lo + i * (C::kQBytes >> 4), kd = k_lo + buf * (C::kTBytes >> 4);
 #pragma unroll
         for (int part = 0; part < (C::kSplitK ? 2 : 1); ++part)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t at = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
-            tc_mma_lo(tmem + i * kN + half * kH, qd + at, kd + part * (C::kTBytes >> 4) + at,
-                      kIdescS, (part | k) != 0);
+            tc_mma_lo(tmem + i * kN, qd + at, kd + part * (C::kTBytes >> 4) + at, kIdescS,
+                      (part | k) != 0);
           }
-        tc_commit(&ctl->s_full[i][half]);
-        if (i == 1 && half == 1) tc_commit(&ctl->k_empty[buf]);
+        tc_commit(&ctl->s_full[i]);
       };
       bool ok = wait_warp(&ctl->q_full[0], 0, ctl, a.status) &&
                 wait_warp(&ctl->q_full[1], 0, ctl, a.status) &&
@@ -740,44 +712,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
         if (leader) {
           scores(0, 0);
           scores(1, 0);
-          if (u.nh > 1) {
-            scores(0, 1);
-            scores(1, 1);
-          }
+          tc_commit(&ctl->k_empty[0]);
         }
       }
-      for (int h = 0; h < u.nh && ok; ++h) {
-        const int j = h >> 1, half = h & 1;
+      for (int j = 0; j < u.nt && ok; ++j) {
         const int vb = C::kVBufs == 2 ? j & 1 : 0;
-        const bool more = h + 2 < u.nh;
-        const uint32_t vd = v_lo + ((vb * C::kTBytes + half * (D * 128)) >> 4);
-        if (half == 0) ok = wait_warp(&ctl->v_full[vb], (j / C::kVBufs) & 1, ctl, a.status);
+        const int kb = C::kKBufs == 2 ? (j + 1) & 1 : 0;  // of the next keys
+        const bool more = j + 1 < u.nt;
+        const uint32_t vd = v_lo + vb * (C::kTBytes >> 4);
+        ok = wait_warp(&ctl->v_full[vb], (j / C::kVBufs) & 1, ctl, a.status);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          ok = ok && wait_warp(&ctl->p_full[i][half], j & 1, ctl, a.status);
+          ok = ok && wait_warp(&ctl->p_full[i], j & 1, ctl, a.status);
           if (!ok) break;
           tc_fence_after();
           if (leader) {
 #pragma unroll
             for (int part = 0; part < (C::kSplitV ? 2 : 1); ++part)
 #pragma unroll
-              for (int k = 0; k < kH / 16; ++k)
-                tc_mma_tmem_a_lo(tmem + 2 * kN + i * 128, tmem + i * kN + half * kH + 8 * k,
-                                 vd + ((part * C::kTBytes + k * 32) >> 4), kIdescO,
-                                 (part | k) != 0 ? 1u : h != 0);
-            tc_commit(&ctl->o_done[i]);
-            if (i == 1 && half == 1) tc_commit(&ctl->v_empty[vb]);
+              for (int k = 0; k < kN / 16; ++k)
+                tc_mma_tmem_a_lo(tmem + 2 * kN + i * 128, tmem + i * kN + 8 * k,
+                                 vd + ((part * C::kTBytes + (k >> 2) * (D * 128) + (k & 3) * 32) >> 4),
+                                 kIdescO, (part | k) != 0 ? 1u : j != 0);
           }
-          if (more) {  // the scores two halves on take the place of the p just read
-            if (i == 0 && half == 0) {
-              const int jk = j + 1;
-              ok = wait_warp(&ctl->k_full[C::kKBufs == 2 ? jk & 1 : 0], (jk / C::kKBufs) & 1, ctl,
-                             a.status);
+          if (more) {
+            if (i == 0) {
+              ok = wait_warp(&ctl->k_full[kb], ((j + 1) / C::kKBufs) & 1, ctl, a.status);
               if (!ok) break;
               tc_fence_after();
             }
-            if (leader) scores(i, h + 2);
+            if (leader) scores(i, kb);
           }
+        }
+        if (!ok) break;
+        if (leader) {
+          tc_commit(&ctl->v_empty[vb]);
+          if (more) tc_commit(&ctl->k_empty[kb]);
         }
       }
       // all issued MMAs have completed once this arrives
