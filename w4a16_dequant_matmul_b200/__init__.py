@@ -475,30 +475,57 @@ def wq_quantize_gptq(W, X, group: int = 128, zero_point: bool = True, damp: floa
     return packed, S, Z
 
 
-_KV4_DTYPES = None
+# The 4-bit KV cache calls are made once or more a decode step on tensors of a few KB, so what
+# the host spends on them counts: names of torch and the library's functions are looked up
+# once, and arguments travel packed.
+_KV4 = None
 
 
-def _kv4_dtype(t, name):
-    global _KV4_DTYPES
-    if _KV4_DTYPES is None:
+class _Kv4Names:
+    """torch's names and the library's functions that the calls below use."""
+
+    def __init__(self):
         import torch
 
-        _KV4_DTYPES = {torch.bfloat16: WQ_BF16, torch.float16: WQ_F16}
-    code = _KV4_DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be bfloat16 or float16")
-    return code
+        self.int32, self.uint8, self.float32 = torch.int32, torch.uint8, torch.float32
+        self.empty = torch.empty_strided
+        self.code = {torch.bfloat16: WQ_BF16, torch.float16: WQ_F16}
+        self.out_code = {torch.float32: WQ_F32, torch.bfloat16: WQ_BF16, torch.float16: WQ_F16}
+        self.device = torch.cuda.device
+        self.current_device = getattr(torch._C, "_cuda_getDevice", None) or \
+            torch.cuda.current_device
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        self.workspace_bytes = {}  # by device
+        handle = lib()
+        self.block_tables = handle.wq_kv4_block_tables
+        self.append = handle.wq_kv4_append
+        self.read = handle.wq_kv4_read
+        self.attention = handle.wq_kv4_attention
 
 
-def _kv4_ints(t, name, shape):
-    """A contiguous int32 tensor of the given shape (None: any size)."""
-    if str(t.dtype) != "torch.int32":
+def _kv4():
+    global _KV4
+    if _KV4 is None:
+        _KV4 = _Kv4Names()
+    return _KV4
+
+
+def _kv4_stream(k, t, stream):
+    """Handle of `stream`, or of the current stream of t's device; None where that device is not
+    the current one (the caller then makes it so and calls itself again)."""
+    d = t.get_device()
+    if d < 0:  # a host tensor: the library rejects it; any stream will do
+        return 0
+    if d != k.current_device():
+        return None
+    return k.raw_stream(d) if stream is None else stream.cuda_stream
+
+
+def _kv4_bad_ints(t, name, n):
+    if t.dtype is not _kv4().int32:
         raise TypeError(f"{name} must be int32")
-    got = tuple(t.shape)
-    if len(got) != len(shape) or any(w is not None and w != n for n, w in zip(got, shape)):
-        raise ValueError(f"{name} has shape {got}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous, of shape {n}, not {tuple(t.shape)}")
 
 
 def _kv4_heads(t, name):
@@ -510,10 +537,27 @@ def _kv4_heads(t, name):
     return n, h, d, st if n > 1 else 0, sh if h > 1 else 0
 
 
+def _kv4_code(t, name):
+    code = _kv4().code.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float16")
+    return code
+
+
+def _kv4_tables(t, B):
+    """Width and row stride of block tables int32 [B, width]."""
+    if t.dtype is not _kv4().int32 or t.dim() != 2 or t.shape[0] != B:
+        raise ValueError("tables must be int32 [B, width]")
+    if t.is_contiguous():
+        width = t.shape[1]
+        return width, width
+    return t.shape[1], _rows(t, "tables")
+
+
 def _kv4_cache(cache, head_dim, group):
-    """(packed wq_kv4_cache, its fields, group) of a cache tensor of wq_kv4_alloc."""
+    """The fields of wq_kv4_cache for a cache tensor of wq_kv4_alloc."""
     group = head_dim if group is None else group
-    if str(cache.dtype) != "torch.uint8" or cache.dim() != 3 or not cache.is_contiguous():
+    if cache.dtype is not _kv4().uint8 or cache.dim() != 3 or not cache.is_contiguous():
         raise ValueError("cache must be a contiguous uint8 [num_blocks, kv_heads, bytes] tensor")
     n, h, chunk = cache.shape
     row = head_dim + 8 * (head_dim // group) if group > 0 else 0
@@ -551,59 +595,76 @@ def wq_kv4_block_tables(ctx_lens, new_lens, free_blocks, tables, block_size: int
     returns (slots int32 [n_slots], q_starts int32 [B + 1], kv_lens int32 [B], taken int32 [1]).
     ctx_lens, new_lens: int32 [B], tokens held and tokens to come. Slots behind the last new
     token are -1."""
-    import torch
-
+    k = _KV4 or _kv4()
+    handle = _kv4_stream(k, ctx_lens, stream)
+    if handle is None:
+        with k.device(ctx_lens.device):
+            return wq_kv4_block_tables(ctx_lens, new_lens, free_blocks, tables, block_size,
+                                       n_slots, stream)
+    i32 = k.int32
     B = ctx_lens.shape[0]
-    _kv4_ints(ctx_lens, "ctx_lens", (B,))
-    _kv4_ints(new_lens, "new_lens", (B,))
-    _kv4_ints(free_blocks, "free_blocks", (None,))
-    if tables.dtype != torch.int32 or tables.dim() != 2 or tables.shape[0] != B:
-        raise ValueError("tables must be int32 [B, width]")
-    ld = _rows(tables, "tables")
-    out = torch.empty((n_slots + 2 * B + 2,), dtype=torch.int32, device=ctx_lens.device)
-    slots, q_starts, kv_lens, taken = out.split((n_slots, B + 1, B, 1))
-    with _on_device(ctx_lens):
-        st = lib().wq_kv4_block_tables(
-            ctx_lens.data_ptr(), new_lens.data_ptr(), B, free_blocks.data_ptr(),
-            free_blocks.shape[0], block_size, tables.data_ptr(), tables.shape[1], ld,
-            slots.data_ptr(), n_slots, q_starts.data_ptr(), kv_lens.data_ptr(), taken.data_ptr(),
-            _stream_handle(ctx_lens, stream))
-    _check(st, "wq_kv4_block_tables")
+    if ctx_lens.dtype is not i32 or ctx_lens.dim() != 1 or not ctx_lens.is_contiguous():
+        _kv4_bad_ints(ctx_lens, "ctx_lens", (B,))
+    if new_lens.dtype is not i32 or new_lens.shape != (B,) or not new_lens.is_contiguous():
+        _kv4_bad_ints(new_lens, "new_lens", (B,))
+    if free_blocks.dtype is not i32 or free_blocks.dim() != 1 or not free_blocks.is_contiguous():
+        _kv4_bad_ints(free_blocks, "free_blocks", ("n",))
+    width, ld = _kv4_tables(tables, B)
+    out = k.empty((n_slots + 2 * B + 2,), (1,), dtype=i32, device=ctx_lens.device)
+    slots, q_starts, kv_lens, taken = out.split_with_sizes((n_slots, B + 1, B, 1))
+    at = out.data_ptr()
+    st = k.block_tables(ctx_lens.data_ptr(), new_lens.data_ptr(), B, free_blocks.data_ptr(),
+                        free_blocks.shape[0], block_size, tables.data_ptr(), width, ld, at,
+                        n_slots, at + 4 * n_slots, at + 4 * (n_slots + B + 1),
+                        at + 4 * (n_slots + 2 * B + 1), handle)
+    if st != 0:
+        raise WQError(st, "wq_kv4_block_tables")
     return slots, q_starts, kv_lens, taken
 
 
 def wq_kv4_append(K, V, slots, cache, group: int = None, stream=None) -> None:
     """Quantize keys and values [T, kv_heads, head_dim] (bfloat16 or float16, any token and head
     strides) into slots (int32 [T], negative: skipped) of the cache."""
+    k = _KV4 or _kv4()
+    handle = _kv4_stream(k, K, stream)
+    if handle is None:
+        with k.device(K.device):
+            return wq_kv4_append(K, V, slots, cache, group, stream)
     T, h, d, kt, kh = _kv4_heads(K, "K")
-    if V.shape != K.shape or V.dtype != K.dtype:
+    if V.shape != K.shape or V.dtype is not K.dtype:
         raise ValueError("K and V must have one shape and dtype")
     _, _, _, vt, vh = _kv4_heads(V, "V")
-    _kv4_ints(slots, "slots", (T,))
+    if slots.dtype is not k.int32 or slots.shape != (T,) or not slots.is_contiguous():
+        _kv4_bad_ints(slots, "slots", (T,))
     c = _kv4_cache(cache, d, group)
     if c[2] != h:
         raise ValueError(f"the cache has {c[2]} KV heads, K has {h}")
-    with _on_device(K):
-        st = lib().wq_kv4_append(K.data_ptr(), V.data_ptr(), _kv4_dtype(K, "K"), T, kt, kh, vt, vh,
-                                 slots.data_ptr(), _KV4_CACHE.pack(*c), _stream_handle(K, stream))
-    _check(st, "wq_kv4_append")
+    st = k.append(K.data_ptr(), V.data_ptr(), _kv4_code(K, "K"), T, kt, kh, vt, vh,
+                  slots.data_ptr(), _KV4_CACHE.pack(*c), handle)
+    if st != 0:
+        raise WQError(st, "wq_kv4_append")
 
 
 def wq_kv4_read(cache, slots, head_dim: int, group: int = None, out_dtype=None, stream=None):
     """Values S'(q - Z) stored in slots (int32 [T]; zeros for negative ones): (K, V), each
     [T, kv_heads, head_dim] float32 (exact), bfloat16 or float16."""
-    import torch
-
-    out_dtype = torch.float32 if out_dtype is None else out_dtype
-    code = {torch.float32: WQ_F32, torch.bfloat16: WQ_BF16, torch.float16: WQ_F16}.get(out_dtype, -1)
-    _kv4_ints(slots, "slots", (None,))
+    k = _KV4 or _kv4()
+    handle = _kv4_stream(k, cache, stream)
+    if handle is None:
+        with k.device(cache.device):
+            return wq_kv4_read(cache, slots, head_dim, group, out_dtype, stream)
+    out_dtype = k.float32 if out_dtype is None else out_dtype
+    if slots.dtype is not k.int32 or slots.dim() != 1 or not slots.is_contiguous():
+        _kv4_bad_ints(slots, "slots", ("T",))
     c = _kv4_cache(cache, head_dim, group)
-    T = slots.shape[0]
-    K, V = torch.empty((2, T, c[2], head_dim), dtype=out_dtype, device=cache.device).unbind(0)
-    with _on_device(cache):
-        st = lib().wq_kv4_read(_KV4_CACHE.pack(*c), slots.data_ptr(), T, K.data_ptr(), V.data_ptr(),
-                               code, _stream_handle(cache, stream))
-    _check(st, "wq_kv4_read")
+    T, h = slots.shape[0], c[2]
+    shape, strides, dev = (T, h, head_dim), (h * head_dim, head_dim, 1), cache.device
+    K = k.empty(shape, strides, dtype=out_dtype, device=dev)
+    V = k.empty(shape, strides, dtype=out_dtype, device=dev)
+    st = k.read(_KV4_CACHE.pack(*c), slots.data_ptr(), T, K.data_ptr(), V.data_ptr(),
+                k.out_code.get(out_dtype, -1), handle)
+    if st != 0:
+        raise WQError(st, "wq_kv4_read")
     return K, V
 
 
@@ -620,34 +681,44 @@ def wq_kv4_attention(Q, cache, tables, q_starts, kv_lens, max_q: int, group: int
     [T, heads]). scale defaults to head_dim ** -0.5; max_q: the largest number of rows of a
     request; window > 0: each row sees the last `window` keys only. Rows outside q_starts are
     left as they were."""
-    import torch
-
+    k = _KV4 or _kv4()
+    handle = _kv4_stream(k, Q, stream)
+    if handle is None:
+        with k.device(Q.device):
+            return wq_kv4_attention(Q, cache, tables, q_starts, kv_lens, max_q, group, scale,
+                                    causal, window, out, return_lse, workspace, stream)
     T, heads, d, qt, qh = _kv4_heads(Q, "Q")
     c = _kv4_cache(cache, d, group)
     B = kv_lens.shape[0]
-    _kv4_ints(kv_lens, "kv_lens", (B,))
-    _kv4_ints(q_starts, "q_starts", (B + 1,))
-    if tables.dtype != torch.int32 or tables.dim() != 2 or tables.shape[0] != B:
-        raise ValueError("tables must be int32 [B, width]")
+    if kv_lens.dtype is not k.int32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous():
+        _kv4_bad_ints(kv_lens, "kv_lens", (B,))
+    if q_starts.dtype is not k.int32 or q_starts.shape != (B + 1,) or not q_starts.is_contiguous():
+        _kv4_bad_ints(q_starts, "q_starts", (B + 1,))
+    width, ld = _kv4_tables(tables, B)
+    dev = Q.device
     if out is None:
-        out = torch.empty((T, heads, d), dtype=Q.dtype, device=Q.device)
         ot, oh = heads * d, d
+        out = k.empty((T, heads, d), (ot, oh, 1), dtype=Q.dtype, device=dev)
     else:
-        if out.shape != Q.shape or out.dtype != Q.dtype:
+        if out.shape != Q.shape or out.dtype is not Q.dtype:
             raise ValueError("out must have Q's shape and dtype")
         _, _, _, ot, oh = _kv4_heads(out, "out")
-    lse = torch.empty((T, heads), dtype=torch.float32, device=Q.device) if return_lse else None
+    lse = None
+    if return_lse:
+        lse = k.empty((T, heads), (heads, 1), dtype=k.float32, device=dev)
     if workspace is None:
-        workspace = torch.empty((wq_kv4_attention_workspace_bytes(),), dtype=torch.uint8,
-                                device=Q.device)
+        n = k.workspace_bytes.get(dev)
+        if n is None:
+            n = k.workspace_bytes[dev] = wq_kv4_attention_workspace_bytes()
+        workspace = k.empty((n,), (1,), dtype=k.uint8, device=dev)
+    else:
+        n = workspace.numel() * workspace.element_size()
     args = _KV4_ATTENTION.pack(
-        Q.data_ptr(), T, qt, qh, *c, tables.data_ptr(), tables.shape[1], _rows(tables, "tables"),
-        q_starts.data_ptr(), kv_lens.data_ptr(), B, out.data_ptr(), ot, oh,
-        0 if lse is None else lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _kv4_dtype(Q, "Q"), heads, int(max_q),
-        1 if causal else 0, int(window), d ** -0.5 if scale is None else float(scale))
-    with _on_device(Q):
-        st = lib().wq_kv4_attention(args, _stream_handle(Q, stream))
+        Q.data_ptr(), T, qt, qh, *c, tables.data_ptr(), width, ld, q_starts.data_ptr(),
+        kv_lens.data_ptr(), B, out.data_ptr(), ot, oh, 0 if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), n, _kv4_code(Q, "Q"), heads, int(max_q), 1 if causal else 0,
+        int(window), d ** -0.5 if scale is None else float(scale))
+    st = k.attention(args, handle)
     if st != 0:
         raise WQError(st, "wq_kv4_attention")
     return (out, lse) if return_lse else out
