@@ -21,8 +21,10 @@
 // sums a unit's parts in CTA order, so results do not depend on timing.
 //
 // Data path. A producer warp streams each tile's blocks by bulk copies (one per block of a
-// head) through an mbarrier ring; four warps take 16 tokens of every tile each, with their own
-// softmax state, joined at the end of a unit.
+// head) through an mbarrier ring, and turns the scale words of the tile that it asked for three
+// tiles ago into the constants of the formulas above, once for all (each consumer lane did that
+// for itself at first: a tenth of all instructions); four warps take 16 tokens of every tile
+// each, with their own softmax state, joined at the end of a unit.
 #include <atomic>
 
 #include "common.cuh"
@@ -36,6 +38,7 @@ namespace {
 constexpr int kTile = 64;   // tokens per tile
 constexpr int kWarps = 4;   // consumer warps, 16 tokens of the tile each
 constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kLag = 3;     // tiles from a copy's issue to the making of its constants
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr float kHeadroom = 8.0f;  // m moves when a score passes it by this
 constexpr float kLift = 7.0f;      // p is taken times 2^kLift
@@ -43,16 +46,22 @@ constexpr float kLift = 7.0f;      // p is taken times 2^kLift
 template <int D, int G, int NT>
 struct Cfg {
   static constexpr int kStageBytes = kTile * (D + 8 * G);
+  // Constants of a token: k1[G], k2[G], lv, 1 / S_v, S_v,g / S_v (G > 1), padded to 16 bytes;
+  // and a word of Z for its values (below).
+  static constexpr int kRec = G == 1 ? 4 : G == 2 ? 8 : 16;
+  static constexpr int kConstBytes = kTile * 4 * (kRec + G);
   static constexpr int kRows = 8 * NT;
-  static constexpr int kStages = 6;
+  static constexpr int kCtasPerSm = NT == 1 && G <= 2 ? 3 : 2;  // by registers and shared memory
+  static constexpr int kStages = D == 128 && G > 1 ? 5 : 6;
   static constexpr int kMergeFloats = 2 * kRows * (D + 1);  // two warps' O rows, padded
-  static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
 };
 
 struct Ctl {
-  uint64_t full[8];
-  uint64_t empty[8];
+  uint64_t full[8];   // a tile's bytes have landed
+  uint64_t ready[8];  // its constants are written
+  uint64_t empty[8];  // the consumers have read both
   uint32_t pieces[8];  // bit i: piece i of the stage's tile is there
+  int32_t left[8];     // keys from the tile's first on
   int64_t scan[kWarps + 1];
   int64_t total;
   int64_t off0;  // tiles of request b0 before this CTA's share
@@ -63,8 +72,9 @@ struct Ctl {
 
 template <int D, int G, int NT>
 constexpr int smem_bytes() {
-  return Cfg<D, G, NT>::kStages * Cfg<D, G, NT>::kStageBytes +
-         Cfg<D, G, NT>::kMergeFloats * 4 + static_cast<int>(sizeof(Ctl));
+  using C = Cfg<D, G, NT>;
+  return C::kStages * (C::kStageBytes + C::kConstBytes) + C::kMergeFloats * 4 +
+         static_cast<int>(sizeof(Ctl));
 }
 
 // What one request asks of this kernel.
@@ -187,7 +197,7 @@ struct Desc {
   int32_t first_row;  // row of the unit's request where the row tile begins, -1: none
   int q0, rows, head;  // request's first row of Q, its rows (tokens x ratio), KV head
   int last_cta;
-  int pad;  // 24 bytes: the parts behind the descriptors stay 8-byte aligned
+  int pad[3];  // 32 bytes: the parts behind the descriptors are 16-byte aligned
 };
 constexpr int kMaxRows = 16;
 __host__ __device__ constexpr int part_floats(int dim) { return kMaxRows * (dim + 2); }
@@ -205,7 +215,8 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   constexpr int KW = D / 32;  // K words of a lane's share of a row; one 32-dim step each
   constexpr int VT = D / 16;  // 16-dim tiles of V: one byte of a lane's share each
   extern __shared__ __align__(128) uint8_t smem[];
-  float* merge = reinterpret_cast<float*>(smem + kStages * C::kStageBytes);
+  uint8_t* consts = smem + kStages * C::kStageBytes;
+  float* merge = reinterpret_cast<float*>(consts + kStages * C::kConstBytes);
   Ctl* ctl = reinterpret_cast<Ctl*>(merge + C::kMergeFloats);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -213,6 +224,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->ready[s], 1);
       mbar_init(&ctl->empty[s], kWarps);
     }
     ctl->abort = 0;
@@ -279,84 +291,163 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   const int npieces = kTile >> piece_log2;
   const int piece_bytes = piece * (D + 8 * G);
 
+  // Position in the line: request, KV head, row tile, tile. The divisions are made once.
+  int b = ctl->b0;
+  Req r = request<kRows>(a, b);
+  int h, rt, t;
+  {
+    const int64_t unit = ctl->off0 / r.nt;
+    t = static_cast<int>(ctl->off0 - unit * r.nt);
+    h = static_cast<int>(unit / r.row_tiles);
+    rt = static_cast<int>(unit - static_cast<int64_t>(h) * r.row_tiles);
+  }
+  int64_t left = end - begin;  // > 0
+  // to the next unit (the caller has tiles left, so there is one)
+  auto next_unit = [&]() {
+    t = 0;
+    if (++rt < r.row_tiles) return;
+    rt = 0;
+    if (++h < kc.kv_heads) return;
+    h = 0;
+    do {
+      r = request<kRows>(a, ++b);
+    } while (r.row_tiles == 0);
+  };
+
   if (warp == kWarps) {
     // ------------------------------------------------------------------ producer warp
-    int b = ctl->b0;
-    int64_t off = ctl->off0, left = end - begin;
+    uint32_t s = 0, phase = 0;    // ring position, and the parity of its fill
+    uint32_t cs = 0, cphase = 0;  // the same of the constants
     uint32_t it = 0;
+    int table_of = -1, first = 0, cached = -1;  // 32 pieces' blocks, read ahead by the lanes
+    const int64_t chunk = kc.chunk_bytes();
+    const int64_t codes = static_cast<int64_t>(kc.block) * (D / 2);
+    const int64_t reach = static_cast<int64_t>(a.width) << kc.block_log2;
+    // (a stage's constants are free when its bytes are: the copy waited for that)
+    auto constants = [&]() -> bool {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&ctl->full[cs], cphase, kLimitNs) && !ctl->abort))
+        return false;
+      const uint32_t there = ctl->pieces[cs];
+      const int keys = ctl->left[cs];
+      const uint8_t* st = smem + cs * C::kStageBytes;
+      float* rec = reinterpret_cast<float*>(consts + cs * C::kConstBytes);
+      uint32_t* zrec = reinterpret_cast<uint32_t*>(rec + kTile * C::kRec);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int tok = lane + 32 * half;
+        const int pc = tok >> piece_log2;
+        const bool in = tok < keys && ((there >> pc) & 1u);
+        const uint32_t* sz = reinterpret_cast<const uint32_t*>(st + pc * piece_bytes + piece * D) +
+                             (tok & (piece - 1)) * G;
+        float c[C::kRec];
+#pragma unroll
+        for (int i = 0; i < C::kRec; ++i) c[i] = 0.0f;
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          const uint32_t ks = in ? sz[i] : 0u, vz = in ? sz[piece * G + i] : 0u;
+          const float sk = f16_bits_to_f32(ks & 0xFFFFu) * a.scale_log2;
+          c[i] = 16.0f * sk;
+          c[G + i] = sk * (16.0f + f16_bits_to_f32(ks >> 16));
+          const float sv = f16_bits_to_f32(vz & 0xFFFFu);
+          if (G > 1) c[2 * G + 2 + i] = sv;
+          top = fmaxf(top, sv);
+          // 1024 + Z (low) and -(64 + Z) as binary16: what the two nibbles of a byte are
+          // expanded with
+          const uint32_t z = vz >> 16;
+          zrec[tok * G + i] = (hfma2(z, 0x3C003C00u, 0x64006400u) & 0xFFFFu) |
+                              hfma2(z, 0xBC00BC00u, 0xD400D400u) << 16;
+        }
+        top = fmaxf(top, 5.9604644775390625e-8f);  // a cache of zeros: S = 0 counts as its value 0
+        c[2 * G] = in ? lg2(top) : -INFINITY;
+        c[2 * G + 1] = 1.0f / top;
+        if (G > 1) {
+#pragma unroll
+          for (int i = 0; i < G; ++i) c[2 * G + 2 + i] *= c[2 * G + 1];
+        }
+#pragma unroll
+        for (int q = 0; q < C::kRec; q += 4)
+          *reinterpret_cast<float4*>(rec + tok * C::kRec + q) =
+              make_float4(c[q], c[q + 1], c[q + 2], c[q + 3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->ready[cs]);
+      if (++cs == kStages) {
+        cs = 0;
+        cphase ^= 1u;
+      }
+      return true;
+    };
     bool ok = true;
-    while (left > 0 && ok) {
-      const Req r = request<kRows>(a, b);
-      const int64_t w = static_cast<int64_t>(kc.kv_heads) * r.row_tiles * r.nt;
-      const int64_t stop = off + left < w ? off + left : w;
-      left -= stop - off;
-      if (r.kv > static_cast<int64_t>(a.width) << kc.block_log2) set_status(a.status, kStRange);
-      const int32_t* table = a.tables + b * a.ld_tables;
-      // the table entries of up to 32 pieces are read ahead by the lanes together
-      int cached_first = -1, cached = -1;
-      for (; off < stop && ok; ++off) {
-        const int64_t unit = off / r.nt;
-        const int h = static_cast<int>(unit / r.row_tiles);
-        const int tile = r.t0 + static_cast<int>(off - unit * r.nt);
-        const int p0 = tile << (6 - piece_log2);  // first piece of the tile
-        if (cached_first < 0 || p0 < cached_first || p0 + npieces > cached_first + 32) {
-          cached_first = p0;
-          const int64_t pos = static_cast<int64_t>(p0 + lane) << piece_log2;
-          const int64_t place = pos >> kc.block_log2;
-          cached = -1;
-          if (pos < r.kv) {
-            if (place < a.width) cached = table[place];
-            if (cached < 0 || cached >= kc.num_blocks) {
-              cached = -1;
-              set_status(a.status, kStRange);
-            }
+    while (true) {
+      const int tile = r.t0 + t;
+      const int p0 = tile << (6 - piece_log2);  // first piece of the tile
+      if (table_of != b || p0 < first || p0 + npieces > first + 32) {
+        if (table_of != b && r.kv > reach) set_status(a.status, kStRange);
+        table_of = b;
+        first = p0;
+        const int64_t pos = static_cast<int64_t>(p0 + lane) << piece_log2;
+        const int64_t place = pos >> kc.block_log2;
+        cached = -1;
+        if (pos < r.kv && place < a.width) {
+          cached = a.tables[b * a.ld_tables + place];
+          if (cached < 0 || cached >= kc.num_blocks) {
+            cached = -1;
+            set_status(a.status, kStRange);
           }
         }
-        const int s = it % kStages;
-        const uint32_t u = it / kStages;
-        const int blk = __shfl_sync(0xffffffffu, cached, (p0 - cached_first + lane) & 31);
-        const bool mine = lane < npieces && blk >= 0;
-        const uint32_t there = __ballot_sync(0xffffffffu, mine);
-        if (u > 0) ok = mbar_wait_bounded(&ctl->empty[s], (u - 1) & 1u, kLimitNs);
+      }
+      const int blk = __shfl_sync(0xffffffffu, cached, (p0 - first + lane) & 31);
+      const bool mine = lane < npieces && blk >= 0;
+      const uint32_t there = __ballot_sync(0xffffffffu, mine);
+      const uint8_t* src = kc.data + (static_cast<int64_t>(blk) * kc.kv_heads + h) * chunk;
+      if (it >= kStages) {
+        ok = mbar_wait_bounded(&ctl->empty[s], phase ^ 1u, kLimitNs);
         ok = __all_sync(0xffffffffu, ok && !ctl->abort);
         if (!ok) break;
-        if (lane == 0) {
-          ctl->pieces[s] = there;
-          mbar_arrive_expect_tx(&ctl->full[s], __popc(there) * piece_bytes);
-        }
-        __syncwarp();
-        if (mine) {
-          uint8_t* dst = smem + s * C::kStageBytes + lane * piece_bytes;
-          const uint8_t* src =
-              kc.data + (static_cast<int64_t>(blk) * kc.kv_heads + h) * kc.chunk_bytes();
-          if (kc.block <= kTile) {
-            bulk_g2s(dst, src, piece_bytes, &ctl->full[s]);
-          } else {  // part of a longer block: its four arrays
-            const int at = (tile * kTile) & (kc.block - 1);
-            const int64_t codes = static_cast<int64_t>(kc.block) * (D / 2);
-            bulk_g2s(dst, src + at * (D / 2), kTile * (D / 2), &ctl->full[s]);
-            bulk_g2s(dst + kTile * (D / 2), src + codes + at * (D / 2), kTile * (D / 2),
-                     &ctl->full[s]);
-            bulk_g2s(dst + kTile * D, src + 2 * codes + at * 4 * G, kTile * 4 * G, &ctl->full[s]);
-            bulk_g2s(dst + kTile * (D + 4 * G), src + 2 * codes + (kc.block + at) * 4 * G,
-                     kTile * 4 * G, &ctl->full[s]);
-          }
-        }
-        ++it;
       }
-      ++b;
-      off = 0;
-    }
-    if (!ok) {
       if (lane == 0) {
-        set_status(a.status, kStTimeout);
-        ctl->abort = 1;
+        ctl->pieces[s] = there;
+        const int64_t n = static_cast<int64_t>(r.kv) - static_cast<int64_t>(tile) * kTile;
+        ctl->left[s] = n < 0 ? 0 : n < kTile ? static_cast<int>(n) : kTile;
+        mbar_arrive_expect_tx(&ctl->full[s], __popc(there) * piece_bytes);
       }
+      __syncwarp();
+      if (mine) {
+        uint8_t* dst = smem + s * C::kStageBytes + lane * piece_bytes;
+        if (kc.block <= kTile) {
+          bulk_g2s(dst, src, piece_bytes, &ctl->full[s]);
+        } else {  // part of a longer block: its four arrays
+          const int at = (tile * kTile) & (kc.block - 1);
+          bulk_g2s(dst, src + at * (D / 2), kTile * (D / 2), &ctl->full[s]);
+          bulk_g2s(dst + kTile * (D / 2), src + codes + at * (D / 2), kTile * (D / 2),
+                   &ctl->full[s]);
+          bulk_g2s(dst + kTile * D, src + 2 * codes + at * 4 * G, kTile * 4 * G, &ctl->full[s]);
+          bulk_g2s(dst + kTile * (D + 4 * G), src + 2 * codes + (kc.block + at) * 4 * G,
+                   kTile * 4 * G, &ctl->full[s]);
+        }
+      }
+      ++it;
+      if (++s == kStages) {
+        s = 0;
+        phase ^= 1u;
+      }
+      if (it > kLag) {
+        ok = constants();
+        if (!ok) break;
+      }
+      if (--left == 0) break;
+      if (++t == r.nt) next_unit();
+    }
+    for (uint32_t q = it > kLag ? it - kLag : 0; ok && q < it; ++q) ok = constants();
+    if (!ok && lane == 0) {
+      set_status(a.status, kStTimeout);
+      ctl->abort = 1;
     }
     // never leave with copies in flight
     if (lane == 0)
-      for (uint32_t s = 0; s < kStages && s < it; ++s)
-        if (!mbar_wait_bounded(&ctl->full[s], ((it - 1 - s) / kStages) & 1u, kLimitNs))
+      for (uint32_t q = 0; q < kStages && q < it; ++q)
+        if (!mbar_wait_bounded(&ctl->full[q], ((it - 1 - q) / kStages) & 1u, kLimitNs))
           set_status(a.status, kStTimeout);
     return;
   }
@@ -368,7 +459,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   auto token_of = [](int rho) { return (rho & 8) + ((rho & 1) ? 4 + (((rho & 7) >> 1) ^ 3) : ((rho & 7) >> 1)); };
   const int tk0 = token_of(g);                        // K rows g (and + 8)
   const int tv0 = token_of(2 * c), tv1 = token_of(2 * c + 1);  // V slots (and + 8)
-  const uint32_t stage0 = smem_u32(smem);
+  const uint32_t stage0 = smem_u32(smem), const0 = smem_u32(consts);
   // the warp's 16 tokens within a stage
   const int wpiece = (16 * warp) >> piece_log2;
   const int wtok = (16 * warp) & (piece - 1);
@@ -378,25 +469,16 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   const uint32_t off_vs = off_ks + piece * 4 * G;
   const int flip0 = (D == 128 && (tv0 & 2)) ? 32 : 0, flip1 = (D == 128 && (tv1 & 2)) ? 32 : 0;
 
-  uint32_t it = 0;
-  int b = ctl->b0;
-  int64_t off = ctl->off0, left = end - begin;
-  int64_t line = begin;  // the line's position of `off`
+  int64_t line = begin;  // the line's position of the unit's tile t
+  uint32_t s = 0, phase = 0;
   bool ok = true;
-  while (left > 0 && ok) {
-    const Req r = request<kRows>(a, b);
-    const int64_t w = static_cast<int64_t>(kc.kv_heads) * r.row_tiles * r.nt;
-    const int64_t stop = off + left < w ? off + left : w;
-    left -= stop - off;
-    const int rows = r.qn * a.ratio;
-    while (off < stop && ok) {
+  while (true) {
+    {
       // ------------------------------------------------ one unit (or this CTA's part of it)
-      const int64_t unit = off / r.nt;
-      const int h = static_cast<int>(unit / r.row_tiles);
-      const int row0 = static_cast<int>(unit - static_cast<int64_t>(h) * r.row_tiles) * kRows;
-      const int u_begin = static_cast<int>(off - unit * r.nt);
-      const int64_t u_stop64 = stop - unit * r.nt;
-      const int u_end = u_stop64 < r.nt ? static_cast<int>(u_stop64) : r.nt;
+      const int rows = r.qn * a.ratio;
+      const int row0 = rt * kRows;
+      const int u_begin = t;
+      const int u_end = left < r.nt - t ? t + static_cast<int>(left) : r.nt;
 
       // Q fragments (B operand), row = 8 n + g, dims 32 j + 8 c .. + 7 per word j
       uint32_t qf[NT][KW][4];
@@ -457,28 +539,27 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
           for (int e = 0; e < 4; ++e) o[n][i][e] = 0.0f;
       }
 
-      for (int t = u_begin; t < u_end; ++t, ++it) {
-        const int s = it % kStages;
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait_bounded(&ctl->full[s], (it / kStages) & 1u, kLimitNs))) {
+      for (int tl = u_begin; tl < u_end; ++tl) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&ctl->full[s], phase, kLimitNs))) {
           set_status(a.status, kStTimeout);
           ctl->abort = 1;
           ok = false;
           break;
         }
         const uint32_t st = stage0 + s * C::kStageBytes;
+        const uint32_t ct = const0 + s * C::kConstBytes;
         const bool there = (ctl->pieces[s] >> wpiece) & 1u;
-        const int pos0 = (r.t0 + t) * kTile + 16 * warp;  // first of the warp's 16 tokens
-        const int nvalid = !there ? 0 : r.kv - pos0;      // tokens of the 16 that exist
-        if (nvalid > 0) {
-          // -- scores: 16 tokens x 8 NT rows
-          float d[NT][G][4];
+        const int pos0 = (r.t0 + tl) * kTile + 16 * warp;        // first of the warp's 16 tokens
+        const bool any = there && ctl->left[s] > 16 * warp;      // some of them exist
+        if (any) {
+          // -- scores: 16 tokens x 8 NT rows; two chains of products each
+          float d[NT][G][4], d2[NT][G][4];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < G; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) d[n][i][e] = 0.0f;
+              for (int e = 0; e < 4; ++e) d[n][i][e] = d2[n][i][e] = 0.0f;
           uint32_t w0[4], w1[4];
           const uint32_t k0 = st + off_k + tk0 * (D / 2) + c * (D / 8);
           if (KW == 4) {
@@ -490,29 +571,18 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
             w0[0] = x.x, w0[1] = x.y;
             w1[0] = y.x, w1[1] = y.y;
           }
-          // the token constants: s = k1 D - k2 X + lv
-          float k1[2][G], k2[2][G], lv[2], isv[2], ratio[2][G];
+          uint32_t wv[4][2];  // the values' codes, of the tokens of the lane's k slots
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int tk = tk0 + 8 * e;
-            const bool in = tk < nvalid;
-            float top = 0.0f;
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-              const uint32_t sz = in ? lds32(st + off_ks + tk * 4 * G + 4 * i) : 0u;
-              const float sk = f16_bits_to_f32(sz & 0xFFFFu) * a.scale_log2;
-              k1[e][i] = 16.0f * sk;
-              k2[e][i] = sk * (16.0f + f16_bits_to_f32(sz >> 16));
-              const uint32_t vz = in ? lds32(st + off_vs + tk * 4 * G + 4 * i) : 0x3C00u;
-              ratio[e][i] = f16_bits_to_f32(vz & 0xFFFFu);
-              top = fmaxf(top, ratio[e][i]);
-            }
-            top = fmaxf(top, 5.9604644775390625e-8f);  // a cache of zeros: S = 0 counts as its value 0
-            lv[e] = in ? lg2(top) : -INFINITY;
-            isv[e] = __fdividef(1.0f, top);
-            if (G > 1) {
-#pragma unroll
-              for (int i = 0; i < G; ++i) ratio[e][i] *= isv[e];
+          for (int e = 0; e < 4; ++e) {
+            const int tv = ((e & 1) ? tv1 : tv0) + 8 * (e >> 1);
+            const uint32_t at = st + off_v + tv * (D / 2) +
+                                ((g * (D / 16)) ^ ((e & 1) ? flip1 : flip0));
+            if (VT == 8) {
+              const uint2 x = lds64(at);
+              wv[e][0] = x.x;
+              wv[e][1] = x.y;
+            } else {
+              wv[e][0] = lds32(at);
             }
           }
 #pragma unroll
@@ -525,9 +595,27 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               mma16<kBf16>(d[n][j * G / KW], fa, qf[n][j][0], qf[n][j][1]);
-              mma16<kBf16>(d[n][j * G / KW], fb, qf[n][j][2], qf[n][j][3]);
+              mma16<kBf16>(d2[n][j * G / KW], fb, qf[n][j][2], qf[n][j][3]);
             }
           }
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(&ctl->ready[s], phase, kLimitNs))) {
+            set_status(a.status, kStTimeout);
+            ctl->abort = 1;
+            ok = false;
+            break;
+          }
+          // the token constants: s = k1 D - k2 X + lv
+          float rec[2][C::kRec];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int q = 0; q < C::kRec; q += 4) {
+              const uint4 x = lds128(ct + ((16 * warp + tk0 + 8 * e) * C::kRec + q) * 4);
+              rec[e][q] = __uint_as_float(x.x);
+              rec[e][q + 1] = __uint_as_float(x.y);
+              rec[e][q + 2] = __uint_as_float(x.z);
+              rec[e][q + 3] = __uint_as_float(x.w);
+            }
           float sc[NT][4];
           bool over = false;
           const bool safe = pos0 + 16 <= safe_end && pos0 >= safe_begin;
@@ -535,10 +623,11 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float v = lv[e >> 1];
+              const float* k = rec[e >> 1];
+              float v = k[2 * G];
 #pragma unroll
               for (int i = 0; i < G; ++i)
-                v += k1[e >> 1][i] * d[n][i][e] - k2[e >> 1][i] * xs[n][i][e & 1];
+                v += k[i] * (d[n][i][e] + d2[n][i][e]) - k[G + i] * xs[n][i][e & 1];
               if (!safe) {
                 const int pos = pos0 + tk0 + 8 * (e >> 1);
                 if (pos > lim[n][e & 1] || (a.window > 0 && pos <= lim[n][e & 1] - a.window))
@@ -578,43 +667,26 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
             for (int e = 0; e < 4; ++e) {
               const float ref = m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1];
               p[e] = ex2(sc[n][e] - ref + kLift);
-              l[n][e & 1] += p[e] * isv[e >> 1];
+              l[n][e & 1] += p[e] * rec[e >> 1][2 * G + 1];
             }
 #pragma unroll
             for (int i = 0; i < G; ++i) {
-              const float r0 = G > 1 ? ratio[0][i] : 1.0f, r1 = G > 1 ? ratio[1][i] : 1.0f;
+              const float r0 = G > 1 ? rec[0][G > 1 ? 2 * G + 2 + i : 0] : 1.0f;
+              const float r1 = G > 1 ? rec[1][G > 1 ? 2 * G + 2 + i : 0] : 1.0f;
               pb[n][i][0] = movmatrix_trans(half2_bits(p[0] * r0, p[1] * r0));
               pb[n][i][1] = movmatrix_trans(half2_bits(p[2] * r1, p[3] * r1));
             }
           }
           // -- O^T += V^T P^T: A rows are dims 16 i + 2 g (and + 1), k slots the tokens
-          uint32_t wv[4][2];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tv = ((e & 1) ? tv1 : tv0) + 8 * (e >> 1);
-            const uint32_t at = st + off_v + tv * (D / 2) +
-                                ((g * (D / 16)) ^ ((e & 1) ? flip1 : flip0));
-            if (VT == 8) {
-              const uint2 x = lds64(at);
-              wv[e][0] = x.x;
-              wv[e][1] = x.y;
-            } else {
-              wv[e][0] = lds32(at);
-            }
-          }
-          uint32_t zlo[G][2], zhi[G][2];  // (1024 + Z) and -(64 + Z) of the slot pairs
+          uint32_t zlo[G][2], zhi[G][2];  // 1024 + Z and -(64 + Z) of the slot pairs
 #pragma unroll
           for (int i = 0; i < G; ++i) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const uint32_t va = lds32(st + off_vs + (tv0 + 8 * q) * 4 * G + 4 * i);
-              const uint32_t vb = lds32(st + off_vs + (tv1 + 8 * q) * 4 * G + 4 * i);
-              // Z of a token that does not exist may be anything: its p is 0, but 0 x NaN is not
-              const uint32_t za = tv0 + 8 * q < nvalid ? va >> 16 : 0u;
-              const uint32_t zb = tv1 + 8 * q < nvalid ? vb & 0xFFFF0000u : 0u;
-              const uint32_t z = za | zb;
-              zlo[i][q] = hfma2(z, 0x3C003C00u, 0x64006400u);       // 1024 + Z
-              zhi[i][q] = hfma2(z, 0xBC00BC00u, 0xD400D400u);       // -Z - 64
+              const uint32_t za = lds32(ct + kTile * 4 * C::kRec + ((16 * warp + tv0 + 8 * q) * G + i) * 4);
+              const uint32_t zb = lds32(ct + kTile * 4 * C::kRec + ((16 * warp + tv1 + 8 * q) * G + i) * 4);
+              zlo[i][q] = __byte_perm(za, zb, 0x5410);
+              zhi[i][q] = __byte_perm(za, zb, 0x7632);
             }
           }
 #pragma unroll
@@ -636,6 +708,10 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->empty[s]);
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
       // a timeout in any warp ends the work of all four (the barriers below need them all, so
       // they have to decide alike)
@@ -761,26 +837,30 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
             d.rows = rows;
             d.head = h;
             // the CTA whose share holds the unit's last tile
-            d.last_cta = static_cast<int>(((line + r.nt) * live + total - 1) / total) - 1;
+            d.last_cta = static_cast<int>(((line - u_begin + r.nt) * live + total - 1) / total) - 1;
             descs[blockIdx.x] = d;
           }
         }
       }
       named_barrier(1, 32 * kWarps);
-      off += u_end - u_begin;
       line += u_end - u_begin;
+      left -= u_end - u_begin;
+      if (left == 0) break;
+      next_unit();
     }
-    ++b;
-    off = 0;
   }
 }
 
-// One row of a unit that several CTAs share: out = sum_i O_i 2^(m_i - m) / l over its parts,
-// in CTA order.
+// One row of a unit that several CTAs share: out = sum_i O_i 2^(m_i - m) / l over its parts i.
+// Four warps take every fourth part, in a fixed order, so that a row of a few hundred parts
+// (one long request) is a few rounds of loads; 16 bytes (8 for 64 dimensions) a lane and part.
+constexpr int kCombineWarps = 4;
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(D) kv4_combine_kernel(const Kv4AttnArgs a, int ctas) {
-  extern __shared__ float weight[];  // one per part
-  __shared__ float red[2][D / 32];
+__global__ void __launch_bounds__(32 * kCombineWarps)
+kv4_combine_kernel(const Kv4AttnArgs a, int ctas) {
+  constexpr int V = D / 32;  // dimensions of a lane
+  __shared__ float acc[kCombineWarps][D];
+  __shared__ float sum[kCombineWarps];
   pdl_wait();
   const Desc* descs = static_cast<const Desc*>(a.workspace);
   const Desc d = descs[blockIdx.x];
@@ -793,39 +873,42 @@ __global__ void __launch_bounds__(D) kv4_combine_kernel(const Kv4AttnArgs a, int
     return parts + (2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0 ? 1 : 0)) * part_floats(D);
   };
   float m = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += D) {
-    const float x = part(i)[kMaxRows * D + row];
-    weight[i] = x;
-    m = fmaxf(m, x);
-  }
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[kMaxRows * D + row]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red[0][warp] = m;
-  __syncthreads();
+  float l = 0.0f, o[V];
 #pragma unroll
-  for (int w = 0; w < D / 32; ++w) m = fmaxf(m, red[0][w]);
-  float l = 0.0f;
-  for (int i = threadIdx.x; i < n; i += D) {
-    const float x = weight[i];
-    const float f = x == -INFINITY ? 1.0f : ex2(x - m);
-    weight[i] = f;
-    l += f * part(i)[kMaxRows * (D + 1) + row];
+  for (int k = 0; k < V; ++k) o[k] = 0.0f;
+#pragma unroll 8
+  for (int i = warp; i < n; i += kCombineWarps) {
+    const float* p = part(i);
+    const float x = p[kMaxRows * D + row];
+    const float f = x == -INFINITY ? 1.0f : ex2(x - m);  // O and l are 0 there, or NaN
+    l += f * p[kMaxRows * (D + 1) + row];
+    float v[V];
+    if (V == 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + row * D + 4 * lane);
+      v[0] = q.x, v[1] = q.y, v[V - 2] = q.z, v[V - 1] = q.w;
+    } else {
+      const float2 q = *reinterpret_cast<const float2*>(p + row * D + 2 * lane);
+      v[0] = q.x, v[1] = q.y;
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] += f * v[k];
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) red[1][warp] = l;
+  for (int k = 0; k < V; ++k) acc[warp][V * lane + k] = o[k];
+  if (lane == 0) sum[warp] = l;
   __syncthreads();
-  l = 0.0f;
-#pragma unroll
-  for (int w = 0; w < D / 32; ++w) l += red[1][w];
-  float o = 0.0f;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) o += weight[i] * part(i)[row * D + threadIdx.x];
+  l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
   const int rr = d.first_row + row;
   const int tok = rr / a.ratio, head = d.head * a.ratio + rr - tok * a.ratio;
-  const float v = l == 0.0f ? 0.0f : o / l;
-  a.out[static_cast<int64_t>(d.q0 + tok) * a.o_tok + static_cast<int64_t>(head) * a.o_head +
-        threadIdx.x] = narrow<kBf16>(v);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* dst = a.out + static_cast<int64_t>(d.q0 + tok) * a.o_tok +
+                  static_cast<int64_t>(head) * a.o_head;
+  const int at = threadIdx.x;
+  if (at < D)
+    dst[at] = narrow<kBf16>(((acc[0][at] + acc[1][at]) + (acc[2][at] + acc[3][at])) * inv);
   if (a.lse && threadIdx.x == 0)
     a.lse[static_cast<int64_t>(d.q0 + tok) * a.heads + head] =
         l == 0.0f ? -INFINITY : (m - kLift + log2f(l)) * 0.6931471805599453f;
@@ -838,6 +921,7 @@ cudaError_t launch_t(const Kv4AttnArgs& a, int sms, cudaStream_t st) {
   using C = Cfg<D, G, NT>;
   static_assert(C::kCtasPerSm <= kMaxCtasPerSm && C::kRows <= kMaxRows, "workspace");
   constexpr int smem = smem_bytes<D, G, NT>();
+  static_assert(C::kCtasPerSm * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
   auto kern = kv4_decode_kernel<D, G, NT, kBf16>;
   static std::atomic<bool> attr[64];
   int dev = 0;
@@ -854,8 +938,7 @@ cudaError_t launch_t(const Kv4AttnArgs& a, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, C::kRows, 1);
-  cfg.blockDim = dim3(D, 1, 1);
-  cfg.dynamicSmemBytes = grid * sizeof(float);
+  cfg.blockDim = dim3(32 * kCombineWarps, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
