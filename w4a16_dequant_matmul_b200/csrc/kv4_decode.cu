@@ -14,7 +14,7 @@
 // 2^8 (p <= 2^15 then); everything else is fp32. With several groups a row, S_v is the
 // largest of the token's and the others enter p as their ratio to it.
 //
-// Work split. The tiles of 64 tokens of all (request, KV head, row tile) units form one line,
+// Work split. The tiles of 128 tokens of all (request, KV head, row tile) units form one line,
 // cut into equal shares, one per CTA, whatever the lengths are: a ragged batch and one long
 // request balance alike, and the host needs no lengths. A share that covers a unit only in
 // part leaves (O, m, l) in the workspace, and a second kernel (programmatic dependent launch)
@@ -23,8 +23,8 @@
 // Data path. A producer warp streams each tile's blocks by bulk copies (one per block of a
 // head) through an mbarrier ring, and turns the scale words of the tile that it asked for three
 // tiles ago into the constants of the formulas above, once for all (each consumer lane did that
-// for itself at first: a tenth of all instructions); four warps take 16 tokens of every tile
-// each, with their own softmax state, joined at the end of a unit.
+// for itself at first: a tenth of all instructions); four warps take 32 tokens of every tile
+// each (two MMA blocks side by side: with one, a warp waited out the latency of every step), with their own softmax state, joined at the end of a unit.
 #include <atomic>
 
 #include "common.cuh"
@@ -35,10 +35,10 @@
 namespace wq {
 namespace {
 
-constexpr int kTile = 64;   // tokens per tile
-constexpr int kWarps = 4;   // consumer warps, 16 tokens of the tile each
+constexpr int kTile = 128;  // tokens per tile
+constexpr int kTileLog2 = 7;
+constexpr int kWarps = 4;   // consumer warps, 32 tokens of the tile each
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kLag = 3;     // tiles from a copy's issue to the making of its constants
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr float kHeadroom = 8.0f;  // m moves when a score passes it by this
 constexpr float kLift = 7.0f;      // p is taken times 2^kLift
@@ -51,8 +51,12 @@ struct Cfg {
   static constexpr int kRec = G == 1 ? 4 : G == 2 ? 8 : 16;
   static constexpr int kConstBytes = kTile * 4 * (kRec + G);
   static constexpr int kRows = 8 * NT;
-  static constexpr int kCtasPerSm = NT == 1 && G <= 2 ? 3 : 2;  // by registers and shared memory
-  static constexpr int kStages = D == 128 && G > 1 ? 5 : 6;
+  // by registers and shared memory
+  static constexpr int kCtasPerSm = NT == 1 && (G == 1 || D == 64) ? 3 : 2;
+  static constexpr int kStages = D == 64 ? 4 : G == 1 && NT == 1 || G == 4 ? 3 : 4;
+  // Tiles from a copy's issue to the making of its constants. The copy waits for a tile kStages
+  // before it, so constants are ready kStages - 1 - kLag tiles ahead of their use.
+  static constexpr int kLag = kStages - 2;
   static constexpr int kMergeFloats = 2 * kRows * (D + 1);  // two warps' O rows, padded
 };
 
@@ -80,7 +84,7 @@ constexpr int smem_bytes() {
 // What one request asks of this kernel.
 struct Req {
   int q0, qn, kv;     // first row of Q, rows, keys
-  int row_tiles, t0, nt;  // row tiles, first 64-token tile, tiles
+  int row_tiles, t0, nt;  // row tiles, first tile of keys, tiles
 };
 
 template <int kRows>
@@ -286,7 +290,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   if (begin == end) return;
 
   const Kv4Cache& kc = a.cache;
-  const int piece_log2 = kc.block_log2 < 6 ? kc.block_log2 : 6;
+  const int piece_log2 = kc.block_log2 < kTileLog2 ? kc.block_log2 : kTileLog2;
   const int piece = 1 << piece_log2;  // tokens of one copied piece
   const int npieces = kTile >> piece_log2;
   const int piece_bytes = piece * (D + 8 * G);
@@ -333,8 +337,8 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
       float* rec = reinterpret_cast<float*>(consts + cs * C::kConstBytes);
       uint32_t* zrec = reinterpret_cast<uint32_t*>(rec + kTile * C::kRec);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int tok = lane + 32 * half;
+      for (int q32 = 0; q32 < kTile / 32; ++q32) {
+        const int tok = lane + 32 * q32;
         const int pc = tok >> piece_log2;
         const bool in = tok < keys && ((there >> pc) & 1u);
         const uint32_t* sz = reinterpret_cast<const uint32_t*>(st + pc * piece_bytes + piece * D) +
@@ -381,7 +385,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
     bool ok = true;
     while (true) {
       const int tile = r.t0 + t;
-      const int p0 = tile << (6 - piece_log2);  // first piece of the tile
+      const int p0 = tile << (kTileLog2 - piece_log2);  // first piece of the tile
       if (table_of != b || p0 < first || p0 + npieces > first + 32) {
         if (table_of != b && r.kv > reach) set_status(a.status, kStRange);
         table_of = b;
@@ -432,14 +436,14 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
         s = 0;
         phase ^= 1u;
       }
-      if (it > kLag) {
+      if (it > C::kLag) {
         ok = constants();
         if (!ok) break;
       }
       if (--left == 0) break;
       if (++t == r.nt) next_unit();
     }
-    for (uint32_t q = it > kLag ? it - kLag : 0; ok && q < it; ++q) ok = constants();
+    for (uint32_t q = it > C::kLag ? it - C::kLag : 0; ok && q < it; ++q) ok = constants();
     if (!ok && lane == 0) {
       set_status(a.status, kStTimeout);
       ctl->abort = 1;
@@ -460,13 +464,14 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   const int tk0 = token_of(g);                        // K rows g (and + 8)
   const int tv0 = token_of(2 * c), tv1 = token_of(2 * c + 1);  // V slots (and + 8)
   const uint32_t stage0 = smem_u32(smem), const0 = smem_u32(consts);
-  // the warp's 16 tokens within a stage
-  const int wpiece = (16 * warp) >> piece_log2;
-  const int wtok = (16 * warp) & (piece - 1);
-  const uint32_t off_k = wpiece * piece_bytes + wtok * (D / 2);
-  const uint32_t off_v = wpiece * piece_bytes + piece * (D / 2) + wtok * (D / 2);
-  const uint32_t off_ks = wpiece * piece_bytes + piece * D + wtok * 4 * G;
-  const uint32_t off_vs = off_ks + piece * 4 * G;
+  // the warp's two blocks of 16 tokens within a stage: their rows of K and of V
+  uint32_t off_k[2], off_v[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int tok = 32 * warp + 16 * w;
+    off_k[w] = (tok >> piece_log2) * piece_bytes + (tok & (piece - 1)) * (D / 2);
+    off_v[w] = off_k[w] + piece * (D / 2);
+  }
   const int flip0 = (D == 128 && (tv0 & 2)) ? 32 : 0, flip1 = (D == 128 && (tv1 & 2)) ? 32 : 0;
 
   int64_t line = begin;  // the line's position of the unit's tile t
@@ -548,101 +553,114 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
         }
         const uint32_t st = stage0 + s * C::kStageBytes;
         const uint32_t ct = const0 + s * C::kConstBytes;
-        const bool there = (ctl->pieces[s] >> wpiece) & 1u;
-        const int pos0 = (r.t0 + tl) * kTile + 16 * warp;        // first of the warp's 16 tokens
-        const bool any = there && ctl->left[s] > 16 * warp;      // some of them exist
-        if (any) {
-          // -- scores: 16 tokens x 8 NT rows; two chains of products each
-          float d[NT][G][4], d2[NT][G][4];
+        const int pos0 = (r.t0 + tl) * kTile + 32 * warp;  // first of the warp's 32 tokens
+        // (tokens of them that do not exist have lv = -inf, and codes of some kind)
+        if (ctl->left[s] > 32 * warp) {
+          // -- scores: two blocks of 16 tokens x 8 NT rows
+          float d[2][NT][G][4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int w = 0; w < 2; ++w)
 #pragma unroll
-            for (int i = 0; i < G; ++i)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) d[n][i][e] = d2[n][i][e] = 0.0f;
-          uint32_t w0[4], w1[4];
-          const uint32_t k0 = st + off_k + tk0 * (D / 2) + c * (D / 8);
-          if (KW == 4) {
-            const uint4 x = lds128(k0), y = lds128(k0 + 8 * (D / 2));
-            w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
-            w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
-          } else {
-            const uint2 x = lds64(k0), y = lds64(k0 + 8 * (D / 2));
-            w0[0] = x.x, w0[1] = x.y;
-            w1[0] = y.x, w1[1] = y.y;
-          }
-          uint32_t wv[4][2];  // the values' codes, of the tokens of the lane's k slots
+              for (int i = 0; i < G; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tv = ((e & 1) ? tv1 : tv0) + 8 * (e >> 1);
-            const uint32_t at = st + off_v + tv * (D / 2) +
-                                ((g * (D / 16)) ^ ((e & 1) ? flip1 : flip0));
-            if (VT == 8) {
-              const uint2 x = lds64(at);
-              wv[e][0] = x.x;
-              wv[e][1] = x.y;
-            } else {
-              wv[e][0] = lds32(at);
+                for (int e = 0; e < 4; ++e) d[w][n][i][e] = 0.0f;
+          uint32_t kw[2][2][4];
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t at = st + off_k[w] + (tk0 + 8 * e) * (D / 2) + c * (D / 8);
+              if (KW == 4) {
+                const uint4 x = lds128(at);
+                kw[w][e][0] = x.x, kw[w][e][1] = x.y, kw[w][e][2] = x.z, kw[w][e][3] = x.w;
+              } else {
+                const uint2 x = lds64(at);
+                kw[w][e][0] = x.x, kw[w][e][1] = x.y;
+              }
             }
-          }
 #pragma unroll
           for (int j = 0; j < KW; ++j) {
-            uint32_t u0[4], u1[4];
-            unpack_hi<kBf16>(w0[j], u0);
-            unpack_hi<kBf16>(w1[j], u1);
-            const uint32_t fa[4] = {u0[0], u1[0], u0[1], u1[1]};
-            const uint32_t fb[4] = {u0[2], u1[2], u0[3], u1[3]};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16<kBf16>(d[n][j * G / KW], fa, qf[n][j][0], qf[n][j][1]);
-              mma16<kBf16>(d2[n][j * G / KW], fb, qf[n][j][2], qf[n][j][3]);
+            for (int w = 0; w < 2; ++w) {
+              uint32_t u0[4], u1[4];
+              unpack_hi<kBf16>(kw[w][0][j], u0);
+              unpack_hi<kBf16>(kw[w][1][j], u1);
+              const uint32_t fa[4] = {u0[0], u1[0], u0[1], u1[1]};
+              const uint32_t fb[4] = {u0[2], u1[2], u0[3], u1[3]};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma16<kBf16>(d[w][n][j * G / KW], fa, qf[n][j][0], qf[n][j][1]);
+                mma16<kBf16>(d[w][n][j * G / KW], fb, qf[n][j][2], qf[n][j][3]);
+              }
             }
           }
+          uint32_t wv[2][4][2];  // the values' codes, of the tokens of the lane's k slots
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tv = ((e & 1) ? tv1 : tv0) + 8 * (e >> 1);
+              const uint32_t at = st + off_v[w] + tv * (D / 2) +
+                                  ((g * (D / 16)) ^ ((e & 1) ? flip1 : flip0));
+              if (VT == 8) {
+                const uint2 x = lds64(at);
+                wv[w][e][0] = x.x;
+                wv[w][e][1] = x.y;
+              } else {
+                wv[w][e][0] = lds32(at);
+              }
+            }
           if (!__all_sync(0xffffffffu, mbar_wait_bounded(&ctl->ready[s], phase, kLimitNs))) {
             set_status(a.status, kStTimeout);
             ctl->abort = 1;
             ok = false;
             break;
           }
-          // the token constants: s = k1 D - k2 X + lv
-          float rec[2][C::kRec];
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int q = 0; q < C::kRec; q += 4) {
-              const uint4 x = lds128(ct + ((16 * warp + tk0 + 8 * e) * C::kRec + q) * 4);
-              rec[e][q] = __uint_as_float(x.x);
-              rec[e][q + 1] = __uint_as_float(x.y);
-              rec[e][q + 2] = __uint_as_float(x.z);
-              rec[e][q + 3] = __uint_as_float(x.w);
-            }
-          float sc[NT][4];
+          // s = k1 D - k2 X + lv, in place of the block's D of group 0
+          float isv[2][2], ratio[2][2][G];
           bool over = false;
-          const bool safe = pos0 + 16 <= safe_end && pos0 >= safe_begin;
+          const bool safe = pos0 + 32 <= safe_end && pos0 >= safe_begin;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+          for (int w = 0; w < 2; ++w)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float* k = rec[e >> 1];
-              float v = k[2 * G];
+            for (int e = 0; e < 2; ++e) {
+              float k[C::kRec];
+              const int tok = 16 * w + tk0 + 8 * e;
 #pragma unroll
-              for (int i = 0; i < G; ++i)
-                v += k[i] * (d[n][i][e] + d2[n][i][e]) - k[G + i] * xs[n][i][e & 1];
-              if (!safe) {
-                const int pos = pos0 + tk0 + 8 * (e >> 1);
-                if (pos > lim[n][e & 1] || (a.window > 0 && pos <= lim[n][e & 1] - a.window))
-                  v = -INFINITY;
+              for (int q = 0; q < C::kRec; q += 4) {
+                const uint4 x = lds128(ct + ((32 * warp + tok) * C::kRec + q) * 4);
+                k[q] = __uint_as_float(x.x);
+                k[q + 1] = __uint_as_float(x.y);
+                k[q + 2] = __uint_as_float(x.z);
+                k[q + 3] = __uint_as_float(x.w);
               }
-              sc[n][e] = v;
-              over |= v > m[n][e & 1] + kHeadroom;
+              isv[w][e] = k[2 * G + 1];
+#pragma unroll
+              for (int i = 0; i < G; ++i) ratio[w][e][i] = G > 1 ? k[G > 1 ? 2 * G + 2 + i : 0] : 1.0f;
+              const int pos = pos0 + tok;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  float v = k[2 * G];
+#pragma unroll
+                  for (int i = 0; i < G; ++i)
+                    v += k[i] * d[w][n][i][2 * e + x] - k[G + i] * xs[n][i][x];
+                  if (!safe && (pos > lim[n][x] || (a.window > 0 && pos <= lim[n][x] - a.window)))
+                    v = -INFINITY;
+                  d[w][n][0][2 * e + x] = v;
+                  over |= v > m[n][x] + kHeadroom;
+                }
             }
-          }
           if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float x = fmaxf(sc[n][e], sc[n][e + 2]);
+                float x = fmaxf(fmaxf(d[0][n][0][e], d[0][n][0][e + 2]),
+                                fmaxf(d[1][n][0][e], d[1][n][0][e + 2]));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -659,51 +677,59 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
             }
           }
           // -- probabilities: binary16 pairs, transposed into the B operand of the V product
-          uint32_t pb[NT][G][2];
+          uint32_t pb[2][NT][G][2];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float p[4];
+            const float r0 = kLift - (m[n][0] == -INFINITY ? 0.0f : m[n][0]);
+            const float r1 = kLift - (m[n][1] == -INFINITY ? 0.0f : m[n][1]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float ref = m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1];
-              p[e] = ex2(sc[n][e] - ref + kLift);
-              l[n][e & 1] += p[e] * rec[e >> 1][2 * G + 1];
-            }
+            for (int w = 0; w < 2; ++w)
 #pragma unroll
-            for (int i = 0; i < G; ++i) {
-              const float r0 = G > 1 ? rec[0][G > 1 ? 2 * G + 2 + i : 0] : 1.0f;
-              const float r1 = G > 1 ? rec[1][G > 1 ? 2 * G + 2 + i : 0] : 1.0f;
-              pb[n][i][0] = movmatrix_trans(half2_bits(p[0] * r0, p[1] * r0));
-              pb[n][i][1] = movmatrix_trans(half2_bits(p[2] * r1, p[3] * r1));
-            }
+              for (int e = 0; e < 2; ++e) {
+                const float p0 = ex2(d[w][n][0][2 * e] + r0), p1 = ex2(d[w][n][0][2 * e + 1] + r1);
+                l[n][0] += p0 * isv[w][e];
+                l[n][1] += p1 * isv[w][e];
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                  pb[w][n][i][e] = movmatrix_trans(
+                      half2_bits(p0 * ratio[w][e][i], p1 * ratio[w][e][i]));
+              }
           }
           // -- O^T += V^T P^T: A rows are dims 16 i + 2 g (and + 1), k slots the tokens
-          uint32_t zlo[G][2], zhi[G][2];  // 1024 + Z and -(64 + Z) of the slot pairs
+          uint32_t zlo[2][G][2], zhi[2][G][2];  // 1024 + Z and -(64 + Z) of the slot pairs
+          const uint32_t zt = ct + kTile * 4 * C::kRec;
 #pragma unroll
-          for (int i = 0; i < G; ++i) {
+          for (int w = 0; w < 2; ++w)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const uint32_t za = lds32(ct + kTile * 4 * C::kRec + ((16 * warp + tv0 + 8 * q) * G + i) * 4);
-              const uint32_t zb = lds32(ct + kTile * 4 * C::kRec + ((16 * warp + tv1 + 8 * q) * G + i) * 4);
-              zlo[i][q] = __byte_perm(za, zb, 0x5410);
-              zhi[i][q] = __byte_perm(za, zb, 0x7632);
-            }
-          }
+            for (int i = 0; i < G; ++i)
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int tok = 32 * warp + 16 * w + 8 * q;
+                const uint32_t za = lds32(zt + ((tok + tv0) * G + i) * 4);
+                const uint32_t zb = lds32(zt + ((tok + tv1) * G + i) * 4);
+                zlo[w][i][q] = __byte_perm(za, zb, 0x5410);
+                zhi[w][i][q] = __byte_perm(za, zb, 0x7632);
+              }
 #pragma unroll
           for (int i = 0; i < VT; ++i) {
             const int gi = i * G / VT;
-            uint32_t fa[4];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              // byte i of the first token in the low half, of the second in the high half
-              const uint32_t y = __byte_perm(wv[2 * q][i >> 2], wv[2 * q + 1][i >> 2],
-                                             static_cast<uint32_t>(i & 3) |
-                                                 (static_cast<uint32_t>(4 + (i & 3)) << 8));
-              fa[2 * q] = hsub2(and_or(y, 0x000F000Fu, 0x64006400u), zlo[gi][q]);
-              fa[2 * q + 1] = hfma2(and_or(y, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zhi[gi][q]);
+            for (int w = 0; w < 2; ++w) {
+              uint32_t fa[4];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                // byte i of the first token in the low half, of the second in the high half
+                const uint32_t y = __byte_perm(wv[w][2 * q][i >> 2], wv[w][2 * q + 1][i >> 2],
+                                               static_cast<uint32_t>(i & 3) |
+                                                   (static_cast<uint32_t>(4 + (i & 3)) << 8));
+                fa[2 * q] = hsub2(and_or(y, 0x000F000Fu, 0x64006400u), zlo[w][gi][q]);
+                fa[2 * q + 1] =
+                    hfma2(and_or(y, 0x00F000F0u, 0x64006400u), 0x2C002C00u, zhi[w][gi][q]);
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_f16_16816(o[n][i], fa, pb[w][n][gi][0], pb[w][n][gi][1]);
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16_16816(o[n][i], fa, pb[n][gi][0], pb[n][gi][1]);
           }
         }
         __syncwarp();
