@@ -16,7 +16,10 @@
 //
 // Work split. The tiles of 128 tokens of all (request, KV head, row tile) units form one line,
 // cut into equal shares, one per CTA, whatever the lengths are: a ragged batch and one long
-// request balance alike, and the host needs no lengths. A share that covers a unit only in
+// request balance alike, and the host needs no lengths. Each unit also has two empty places on
+// the line before its tiles, which is about what its beginning and end cost a CTA: without them,
+// CTAs with the short requests of a batch came in last (64 requests of up to 8192 keys: 108 us
+// with no, 99 / 98 / 100 with 1 / 2 / 3 places; 48 short ones of up to 3001: 62, 47 / 43 / 41). A share that covers a unit only in
 // part leaves (O, m, l) in the workspace, and a second kernel (programmatic dependent launch)
 // sums a unit's parts in CTA order, so results do not depend on timing.
 //
@@ -37,6 +40,7 @@ namespace {
 
 constexpr int kTile = 128;  // tokens per tile
 constexpr int kTileLog2 = 7;
+constexpr int kUnitCost = 2;  // places of a unit on the line before its first tile
 constexpr int kWarps = 4;   // consumer warps, 32 tokens of the tile each
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr uint64_t kLimitNs = 2000000000ull;
@@ -85,6 +89,9 @@ constexpr int smem_bytes() {
 struct Req {
   int q0, qn, kv;     // first row of Q, rows, keys
   int row_tiles, t0, nt;  // row tiles, first tile of keys, tiles
+  __device__ int64_t places(int kv_heads) const {
+    return static_cast<int64_t>(kv_heads) * row_tiles * (nt + kUnitCost);
+  }
 };
 
 template <int kRows>
@@ -244,7 +251,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
     int64_t mine = 0;
     for (int64_t b = r0; b < r0 + per && b < a.requests; ++b) {
       const Req r = request<kRows>(a, static_cast<int>(b));
-      mine += static_cast<int64_t>(a.cache.kv_heads) * r.row_tiles * r.nt;
+      mine += r.places(a.cache.kv_heads);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -273,7 +280,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
       int b = static_cast<int>(r0);
       while (true) {
         const Req r = request<kRows>(a, b);
-        const int64_t w = static_cast<int64_t>(a.cache.kv_heads) * r.row_tiles * r.nt;
+        const int64_t w = r.places(a.cache.kv_heads);
         if (off < w) break;
         off -= w;
         ++b;
@@ -299,23 +306,35 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   int b = ctl->b0;
   Req r = request<kRows>(a, b);
   int h, rt, t;
+  int64_t left = end - begin;  // places from the tile's on
+  int64_t line = begin;        // the unit's first place
   {
-    const int64_t unit = ctl->off0 / r.nt;
-    t = static_cast<int>(ctl->off0 - unit * r.nt);
+    const int64_t unit = ctl->off0 / (r.nt + kUnitCost);
+    const int place = static_cast<int>(ctl->off0 - unit * (r.nt + kUnitCost));
     h = static_cast<int>(unit / r.row_tiles);
     rt = static_cast<int>(unit - static_cast<int64_t>(h) * r.row_tiles);
+    t = place - kUnitCost;
+    line -= place;
+    if (t < 0) {
+      left += t;
+      t = 0;
+    }
   }
-  int64_t left = end - begin;  // > 0
-  // to the next unit (the caller has tiles left, so there is one)
-  auto next_unit = [&]() {
+  if (left <= 0) return;  // no tile in the share
+  // to the next unit; false if no tile of it is in the share
+  auto next_unit = [&]() -> bool {
+    line += r.nt + kUnitCost;
+    left -= kUnitCost;
+    if (left <= 0) return false;
     t = 0;
-    if (++rt < r.row_tiles) return;
+    if (++rt < r.row_tiles) return true;
     rt = 0;
-    if (++h < kc.kv_heads) return;
+    if (++h < kc.kv_heads) return true;
     h = 0;
     do {
       r = request<kRows>(a, ++b);
     } while (r.row_tiles == 0);
+    return true;
   };
 
   if (warp == kWarps) {
@@ -441,7 +460,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
         if (!ok) break;
       }
       if (--left == 0) break;
-      if (++t == r.nt) next_unit();
+      if (++t == r.nt && !next_unit()) break;
     }
     for (uint32_t q = it > C::kLag ? it - C::kLag : 0; ok && q < it; ++q) ok = constants();
     if (!ok && lane == 0) {
@@ -474,7 +493,6 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   }
   const int flip0 = (D == 128 && (tv0 & 2)) ? 32 : 0, flip1 = (D == 128 && (tv1 & 2)) ? 32 : 0;
 
-  int64_t line = begin;  // the line's position of the unit's tile t
   uint32_t s = 0, phase = 0;
   bool ok = true;
   while (true) {
@@ -863,16 +881,15 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
             d.rows = rows;
             d.head = h;
             // the CTA whose share holds the unit's last tile
-            d.last_cta = static_cast<int>(((line - u_begin + r.nt) * live + total - 1) / total) - 1;
+            d.last_cta =
+                static_cast<int>(((line + kUnitCost + r.nt) * live + total - 1) / total) - 1;
             descs[blockIdx.x] = d;
           }
         }
       }
       named_barrier(1, 32 * kWarps);
-      line += u_end - u_begin;
       left -= u_end - u_begin;
-      if (left == 0) break;
-      next_unit();
+      if (left == 0 || !next_unit()) break;
     }
   }
 }
