@@ -614,22 +614,6 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
               }
             }
           }
-          uint32_t wv[2][4][2];  // the values' codes, of the tokens of the lane's k slots
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int tv = ((e & 1) ? tv1 : tv0) + 8 * (e >> 1);
-              const uint32_t at = st + off_v[w] + tv * (D / 2) +
-                                  ((g * (D / 16)) ^ ((e & 1) ? flip1 : flip0));
-              if (VT == 8) {
-                const uint2 x = lds64(at);
-                wv[w][e][0] = x.x;
-                wv[w][e][1] = x.y;
-              } else {
-                wv[w][e][0] = lds32(at);
-              }
-            }
           if (!__all_sync(0xffffffffu, mbar_wait_bounded(&ctl->ready[s], phase, kLimitNs))) {
             set_status(a.status, kStTimeout);
             ctl->abort = 1;
@@ -714,6 +698,22 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
               }
           }
           // -- O^T += V^T P^T: A rows are dims 16 i + 2 g (and + 1), k slots the tokens
+          uint32_t wv[2][4][2];  // the values' codes, of the tokens of the lane's k slots
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tv = ((e & 1) ? tv1 : tv0) + 8 * (e >> 1);
+              const uint32_t at = st + off_v[w] + tv * (D / 2) +
+                                  ((g * (D / 16)) ^ ((e & 1) ? flip1 : flip0));
+              if (VT == 8) {
+                const uint2 x = lds64(at);
+                wv[w][e][0] = x.x;
+                wv[w][e][1] = x.y;
+              } else {
+                wv[w][e][0] = lds32(at);
+              }
+            }
           uint32_t zlo[2][G][2], zhi[2][G][2];  // 1024 + Z and -(64 + Z) of the slot pairs
           const uint32_t zt = ct + kTile * 4 * C::kRec;
 #pragma unroll
@@ -894,24 +894,26 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   }
 }
 
-// One row of a unit that several CTAs share: out = sum_i O_i 2^(m_i - m) / l over its parts i.
-// Four warps take every fourth part, in a fixed order, so that a row of a few hundred parts
-// (one long request) is a few rounds of loads; 16 bytes (8 for 64 dimensions) a lane and part.
-constexpr int kCombineWarps = 4;
+// A unit that several CTAs share: out = sum_i O_i 2^(m_i - m) / l over its parts i, one CTA for
+// four of its rows. kSplit warps of a row take every kSplit-th part, in a fixed order, so that a row of
+// a few hundred parts (one long request) is a few rounds of loads; 16 bytes (8 for 64
+// dimensions) a lane and part.
+constexpr int kJoinRows = 4;
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(32 * kCombineWarps)
+__global__ void __launch_bounds__(512)
 kv4_combine_kernel(const Kv4AttnArgs a, int ctas) {
   constexpr int V = D / 32;  // dimensions of a lane
-  __shared__ float acc[kCombineWarps][D];
-  __shared__ float sum[kCombineWarps];
+  constexpr int kRows = kJoinRows, kSplit = 16 / kRows;
+  __shared__ float acc[kRows][kSplit][D];
+  __shared__ float sum[kRows][kSplit];
   pdl_wait();
   const Desc* descs = static_cast<const Desc*>(a.workspace);
   const Desc d = descs[blockIdx.x];
-  const int row = blockIdx.y;
-  if (d.first_row < 0 || d.first_row + row >= d.rows) return;
+  if (d.first_row < 0 || d.first_row + kRows * static_cast<int>(blockIdx.y) >= d.rows) return;
   const float* parts = reinterpret_cast<const float*>(descs + ctas);
   const int n = d.last_cta - static_cast<int>(blockIdx.x) + 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) / kRows;
+  const int local = (threadIdx.x >> 5) % kRows, row = kRows * blockIdx.y + local;
   auto part = [&](int i) {  // the first CTA's last unit, the others' first
     return parts + (2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0 ? 1 : 0)) * part_floats(D);
   };
@@ -923,7 +925,7 @@ kv4_combine_kernel(const Kv4AttnArgs a, int ctas) {
 #pragma unroll
   for (int k = 0; k < V; ++k) o[k] = 0.0f;
 #pragma unroll 8
-  for (int i = warp; i < n; i += kCombineWarps) {
+  for (int i = warp; i < n; i += kSplit) {
     const float* p = part(i);
     const float x = p[kMaxRows * D + row];
     const float f = x == -INFINITY ? 1.0f : ex2(x - m);  // O and l are 0 there, or NaN
@@ -940,19 +942,29 @@ kv4_combine_kernel(const Kv4AttnArgs a, int ctas) {
     for (int k = 0; k < V; ++k) o[k] += f * v[k];
   }
 #pragma unroll
-  for (int k = 0; k < V; ++k) acc[warp][V * lane + k] = o[k];
-  if (lane == 0) sum[warp] = l;
+  for (int k = 0; k < V; ++k) acc[local][warp][V * lane + k] = o[k];
+  if (lane == 0) sum[local][warp] = l;
   __syncthreads();
-  l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
   const int rr = d.first_row + row;
+  if (warp > 0 || rr >= d.rows) return;
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kSplit; ++w) l += sum[local][w];
   const int tok = rr / a.ratio, head = d.head * a.ratio + rr - tok * a.ratio;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* dst = a.out + static_cast<int64_t>(d.q0 + tok) * a.o_tok +
-                  static_cast<int64_t>(head) * a.o_head;
-  const int at = threadIdx.x;
-  if (at < D)
-    dst[at] = narrow<kBf16>(((acc[0][at] + acc[1][at]) + (acc[2][at] + acc[3][at])) * inv);
-  if (a.lse && threadIdx.x == 0)
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(d.q0 + tok) * a.o_tok +
+                                              static_cast<int64_t>(head) * a.o_head);
+#pragma unroll
+  for (int k = 0; k < V; k += 2) {
+    float x = 0.0f, y = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSplit; ++w) {
+      x += acc[local][w][V * lane + k];
+      y += acc[local][w][V * lane + k + 1];
+    }
+    dst[(V * lane + k) >> 1] = narrow<kBf16>(x * inv) | static_cast<uint32_t>(narrow<kBf16>(y * inv)) << 16;
+  }
+  if (a.lse && lane == 0)
     a.lse[static_cast<int64_t>(d.q0 + tok) * a.heads + head] =
         l == 0.0f ? -INFINITY : (m - kLift + log2f(l)) * 0.6931471805599453f;
 }
@@ -980,8 +992,8 @@ cudaError_t launch_t(const Kv4AttnArgs& a, int sms, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, C::kRows, 1);
-  cfg.blockDim = dim3(32 * kCombineWarps, 1, 1);
+  cfg.gridDim = dim3(grid, C::kRows / kJoinRows, 1);
+  cfg.blockDim = dim3(512, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
