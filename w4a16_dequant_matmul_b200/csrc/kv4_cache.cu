@@ -152,90 +152,140 @@ __device__ __forceinline__ float2 widen(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// One thread holds 8 consecutive dimensions of a row (one 16-byte load, one 32-bit word of
-// codes); the D/8 threads of a row are neighbours, the group's range is reduced among its
-// group/8 of them by shuffles. S', Z and the codes are decided exactly, as in quantize.cu.
-// Bound by HBM: 2 B an element in, D/2 + 4 D/g bytes a row out. K words are stored whole, V
-// bytes one by one (the V order spreads a row's neighbouring bytes over the lanes' shares);
-// both stay within the row, whose sectors L2 puts together.
-template <bool kBf16>
-__global__ void __launch_bounds__(256) append_kernel(Kv4AppendArgs a) {
-  const Kv4Cache c = a.cache;
-  const int lanes = c.dim >> 3, glanes = c.group >> 3;
-  const int rows_per_cta = 256 / lanes;
-  const int sub = threadIdx.x / lanes, w = threadIdx.x - sub * lanes;
-  const int64_t rows = a.tokens * c.kv_heads * 2;  // K and V rows of a (token, head) side by side
-  const int64_t limit = c.num_blocks << c.block_log2;
-  bool range = false, nonfinite = false;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * rows_per_cta + sub;
-       r - sub < rows;  // the same trip count for a whole warp: the shuffles need every lane
-       r += static_cast<int64_t>(gridDim.x) * rows_per_cta) {
-    const bool in = r < rows;
-    const bool is_v = r & 1;
-    const int64_t th = r >> 1;
-    const int64_t tok = th / c.kv_heads;
-    const int head = static_cast<int>(th - tok * c.kv_heads);
-    int slot = in ? a.slots[tok] : -1;
-    if (slot >= limit) {
-      range = true;
-      slot = -1;
+// Codes of 8 weights v of a finite group (|v / S'| < 32 then), as round-half-even of the exact
+// quotient plus Z, clipped to [0, 15], without a test per weight. With w = M_w 2^a and
+// S' = M_s 2^b (M_w < 2^11 for bf16 and binary16, M_s < 2^11, both odd) the quotient is either a
+// half-integer or more than 2^-12 away from every half-integer: for a >= b - 1 the difference
+// has the denominator 2 M_s; for d = b - a > 1 a quotient near k + 1/2 means
+// M_w ~ (2k + 1) M_s 2^(d-1), so the denominator M_s 2^d is at most 2^12. The product with
+// RN(1/S') is within 2^-19 of it, and one FMA onto the 2^-13 grid (floats in [1024, 2048)) puts
+// a half-integer on itself and leaves the others on their side. Adding 1.5 2^23 - 1536 + Ze, Ze
+// the zero-point rounded up to even, rounds to an integer with ties to even k; the low byte is
+// code + (Z & 1).
+__device__ __forceinline__ uint32_t encode8_snap(const float2 (&v)[4], const AsymScale& sz) {
+  const float z1 = static_cast<float>(static_cast<int>(sz.z) & 1);
+  const float lo = 12582912.0f + z1, hi = lo + 15.0f;
+  const float2 inv2 = make_float2(sz.inv_s, sz.inv_s), g2 = make_float2(1536.0f, 1536.0f);
+  const float cz = 12581376.0f + (sz.z + z1);
+  const float2 c2 = make_float2(cz, cz);
+  uint32_t t[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = __fadd2_rn(__ffma2_rn(v[j], inv2, g2), c2);
+    t[2 * j] = __float_as_uint(fminf(fmaxf(x.x, lo), hi));
+    t[2 * j + 1] = __float_as_uint(fminf(fmaxf(x.y, lo), hi));
+  }
+  const uint32_t ev = __byte_perm(__byte_perm(t[0], t[2], 0x0040), __byte_perm(t[4], t[6], 0x0040), 0x5410);
+  const uint32_t od = __byte_perm(__byte_perm(t[1], t[3], 0x0040), __byte_perm(t[5], t[7], 0x0040), 0x5410);
+  return ev + (od << 4) - (static_cast<uint32_t>(sz.z) & 1u) * 0x11111111u;
+}
+
+// 4 x 4 bytes over the four lanes whose numbers differ in bits 1 and 2 only: lane j of them
+// (those two bits) gives up its bytes for byte j of each. Its own inverse.
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane) {
+  uint32_t t = __shfl_xor_sync(0xffffffffu, w, 2);
+  w = __byte_perm(w, t, lane & 2 ? 0x3715 : 0x6240);
+  t = __shfl_xor_sync(0xffffffffu, w, 4);
+  return __byte_perm(w, t, lane & 4 ? 0x3276 : 0x5410);
+}
+
+// Byte offset within its row of the 32-bit word that lane w of a row's D/8 holds: of K, word w
+// of the dimensions' order (4 j + c is stored at c (D/32) + j); of V, after transpose_bytes,
+// byte column g = 4 (w & 1) + (w >> 1 & 3), rows 4 (w >> 3) .. + 3 (bytes 8 i + g of the
+// dimensions' order are stored at g (D/16) + i).
+template <int D>
+__device__ __forceinline__ int word_place(bool is_v, int w, int t) {
+  if (!is_v) return 4 * ((w & 3) * (D / 32) + (w >> 2));
+  const int at = (4 * (w & 1) + ((w >> 1) & 3)) * (D / 16) + 4 * (w >> 3);
+  return D == 128 && (t & 2) ? at ^ 32 : at;
+}
+
+// The (token, head) pairs that a warp's lanes work on: 128 / D of them at a time, the D/8 lanes
+// of a K row and of its V row side by side. Pairs are stepped through without divisions.
+template <int D>
+struct Pairs {
+  static constexpr int kLanes = D / 8, kPerWarp = 16 / kLanes;
+  int64_t tok, step_tok;
+  int head, step_head, heads;
+  __device__ Pairs(int kv_heads, int lane) : heads(kv_heads) {
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) +
+                           (threadIdx.x >> 5)) * kPerWarp + lane / (2 * kLanes);
+    const int64_t step = warps * kPerWarp;
+    tok = first / heads;
+    head = static_cast<int>(first - tok * heads);
+    step_tok = step / heads;
+    step_head = static_cast<int>(step - step_tok * heads);
+  }
+  __device__ void next() {
+    tok += step_tok;
+    head += step_head;
+    if (head >= heads) {
+      head -= heads;
+      ++tok;
     }
-    const bool live = slot >= 0;
+  }
+};
+
+// One lane holds 8 consecutive dimensions of a row (one 16-byte load, one 32-bit word of codes);
+// the group's range is reduced among its group/8 lanes by shuffles. S', Z and the codes are
+// decided exactly, as in quantize.cu. V's words are formed by a byte transpose among four lanes,
+// so that every store is a word. Bound by HBM: 2 B an element in, D/2 + 4 D/g bytes a row out.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(256) append_kernel(Kv4AppendArgs a) {
+  using P = Pairs<D>;
+  const Kv4Cache c = a.cache;
+  const int lane = threadIdx.x & 31;
+  const int glanes = c.group >> 3, groups = c.groups();
+  const bool is_v = (lane / P::kLanes) & 1;
+  const int w = lane % P::kLanes;
+  const int64_t limit = c.num_blocks << c.block_log2;
+  const int64_t chunk_bytes = c.chunk_bytes();
+  const int64_t codes = static_cast<int64_t>(c.block) * (D / 2);
+  const uint16_t* base = (is_v ? a.V : a.K) + 8 * w;
+  const int64_t s_tok = is_v ? a.v_tok : a.k_tok, s_head = is_v ? a.v_head : a.k_head;
+  bool range = false, nonfinite = false;
+  // the trip count is the same for a whole warp: the shuffles need every lane
+  for (P p(c.kv_heads, lane); __any_sync(0xffffffffu, p.tok < a.tokens); p.next()) {
+    int slot = -1;
     uint4 x = make_uint4(0, 0, 0, 0);
-    if (live) {
-      const uint16_t* src = is_v ? a.V + tok * a.v_tok + head * a.v_head
-                                 : a.K + tok * a.k_tok + head * a.k_head;
-      x = ld_stream_u4(src + 8 * w);
+    if (p.tok < a.tokens) {
+      x = ld_stream_u4(base + p.tok * s_tok + p.head * s_head);
+      slot = __ldg(a.slots + p.tok);
+      if (slot >= limit) {
+        range = true;
+        slot = -1;
+      }
     }
     const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-    float v[8];
+    float2 v[4];
     float mn = 0.0f, mx = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = widen<kBf16>(xs[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-      mn = fmin_nan(mn, fmin_nan(f.x, f.y));
-      mx = fmax_nan(mx, fmax_nan(f.x, f.y));
+      v[i] = widen<kBf16>(xs[i]);
+      mn = fmin_nan(mn, fmin_nan(v[i].x, v[i].y));
+      mx = fmax_nan(mx, fmax_nan(v[i].x, v[i].y));
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      const float omn = __shfl_xor_sync(0xffffffffu, mn, o);
-      const float omx = __shfl_xor_sync(0xffffffffu, mx, o);
+    for (int o = 1; o < 16; o <<= 1) {
       if (o < glanes) {
-        mn = fmin_nan(mn, omn);
-        mx = fmax_nan(mx, omx);
+        mn = fmin_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       }
     }
-    if (!live) continue;
     const AsymScale sz = asym_scale_zero(mn, mx);
-    uint32_t word = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float q = sz.bad ? 0.0f : rne_quotient(v[i], sz.s, sz.inv_s) + sz.z;
-      q = fminf(fmaxf(q, 0.0f), 15.0f);
-      word |= static_cast<uint32_t>(__float2int_rz(q)) << (4 * i);
-    }
-    const int half = c.dim >> 1;
+    uint32_t word = sz.bad ? 0u : encode8_snap(v, sz);
+    const uint32_t turned = transpose_bytes(word, lane);
+    if (slot < 0) continue;
+    if (is_v) word = turned;
     const int t = slot & (c.block - 1);
-    uint8_t* chunk = c.data + (static_cast<int64_t>(slot >> c.block_log2) * c.kv_heads + head) *
-                                  c.chunk_bytes();
-    uint8_t* row = chunk + (is_v ? c.block * half : 0) + t * half;
-    if (!is_v) {
-      const int at = (w & 3) * (c.dim >> 5) + (w >> 2);
-      *reinterpret_cast<uint32_t*>(row + 4 * at) = word;
-    } else {
-      const int flip = (c.dim == 128 && (t & 2)) ? 32 : 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = 4 * w + i;  // byte of the natural order
-        row[((n & 7) * (c.dim >> 4) + (n >> 3)) ^ flip] = static_cast<uint8_t>(word >> (8 * i));
-      }
-    }
+    uint8_t* chunk = c.data + (static_cast<int64_t>(slot >> c.block_log2) * c.kv_heads + p.head) *
+                                  chunk_bytes;
+    *reinterpret_cast<uint32_t*>(chunk + (is_v ? codes : 0) + t * (D / 2) +
+                                 word_place<D>(is_v, w, t)) = word;
     if (w % glanes == 0) {
-      const int g = w / glanes, groups = c.groups();
-      uint32_t* szp = reinterpret_cast<uint32_t*>(chunk + 2 * c.block * half) +
-                      (is_v ? c.block * groups : 0) + t * groups + g;
+      uint32_t* szp = reinterpret_cast<uint32_t*>(chunk + 2 * codes) +
+                      (is_v ? c.block * groups : 0) + t * groups + w / glanes;
       *szp = sz.sbits | f32_to_f16_bits(sz.z) << 16;
       if (sz.bad) nonfinite = true;
     }
@@ -244,55 +294,45 @@ __global__ void __launch_bounds__(256) append_kernel(Kv4AppendArgs a) {
   if (nonfinite) set_status(a.status, kStNonFinite);
 }
 
-// The inverse: one thread gives 8 consecutive values S'(q - Z) of a row (exact in fp32, or
+// The inverse: one lane gives 8 consecutive values S'(q - Z) of a row (exact in fp32, or
 // rounded once to 16 bits); slot < 0 gives zeros. Bound by HBM: the values written.
-template <int kOut>  // WQ_F32, WQ_BF16, WQ_F16
+template <int D, int kOut>  // kOut: WQ_F32, WQ_BF16, WQ_F16
 __global__ void __launch_bounds__(256) read_kernel(Kv4ReadArgs a) {
+  using P = Pairs<D>;
   const Kv4Cache c = a.cache;
-  const int lanes = c.dim >> 3;
+  const int lane = threadIdx.x & 31;
+  const bool is_v = (lane / P::kLanes) & 1;
+  const int w = lane % P::kLanes;
   const int64_t limit = c.num_blocks << c.block_log2;
-  const int64_t total = a.tokens * c.kv_heads * 2 * lanes;
+  const int64_t chunk_bytes = c.chunk_bytes();
+  const int64_t codes = static_cast<int64_t>(c.block) * (D / 2);
+  const int groups = c.groups(), my_group = 8 * w / c.group;
   bool range = false;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = i / lanes;
-    const int w = static_cast<int>(i - r * lanes);
-    const int64_t rows = a.tokens * c.kv_heads;
-    const bool is_v = r >= rows;
-    const int64_t th = is_v ? r - rows : r;
-    const int64_t tok = th / c.kv_heads;
-    const int head = static_cast<int>(th - tok * c.kv_heads);
-    int slot = a.slots[tok];
+  for (P p(c.kv_heads, lane); __any_sync(0xffffffffu, p.tok < a.tokens); p.next()) {
+    const bool in = p.tok < a.tokens;
+    int slot = in ? __ldg(a.slots + p.tok) : -1;
     if (slot >= limit) {
       range = true;
       slot = -1;
     }
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    uint32_t word = 0, sz = 0;
     if (slot >= 0) {
-      const int half = c.dim >> 1, t = slot & (c.block - 1);
+      const int t = slot & (c.block - 1);
       const uint8_t* chunk =
-          c.data + (static_cast<int64_t>(slot >> c.block_log2) * c.kv_heads + head) *
-                       c.chunk_bytes();
-      const uint8_t* row = chunk + (is_v ? c.block * half : 0) + t * half;
-      uint32_t word = 0;
-      if (!is_v) {
-        word = *reinterpret_cast<const uint32_t*>(row + 4 * ((w & 3) * (c.dim >> 5) + (w >> 2)));
-      } else {
-        const int flip = (c.dim == 128 && (t & 2)) ? 32 : 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = 4 * w + j;
-          word |= static_cast<uint32_t>(row[((n & 7) * (c.dim >> 4) + (n >> 3)) ^ flip]) << (8 * j);
-        }
-      }
-      const int groups = c.groups();
-      const uint32_t sz = *(reinterpret_cast<const uint32_t*>(chunk + 2 * c.block * half) +
-                            (is_v ? c.block * groups : 0) + t * groups + 8 * w / c.group);
-      const float s = f16_bits_to_f32(sz & 0xFFFFu), z = f16_bits_to_f32(sz >> 16);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = s * (static_cast<float>((word >> (4 * j)) & 15u) - z);
+          c.data + (static_cast<int64_t>(slot >> c.block_log2) * c.kv_heads + p.head) * chunk_bytes;
+      word = __ldg(reinterpret_cast<const uint32_t*>(chunk + (is_v ? codes : 0) + t * (D / 2) +
+                                                     word_place<D>(is_v, w, t)));
+      sz = __ldg(reinterpret_cast<const uint32_t*>(chunk + 2 * codes) +
+                 (is_v ? c.block * groups : 0) + t * groups + my_group);
     }
-    const int64_t at = th * c.dim + 8 * w;
+    const uint32_t turned = transpose_bytes(word, lane);
+    if (!in) continue;
+    if (is_v) word = turned;
+    const float s = f16_bits_to_f32(sz & 0xFFFFu), z = f16_bits_to_f32(sz >> 16);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = s * (static_cast<float>((word >> (4 * j)) & 15u) - z);
+    const int64_t at = (p.tok * c.kv_heads + p.head) * D + 8 * w;
     if (kOut == WQ_F32) {
       float4* dst = reinterpret_cast<float4*>(static_cast<float*>(is_v ? a.V : a.K) + at);
       dst[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -327,23 +367,37 @@ cudaError_t launch_kv4_block_tables(const Kv4TablesArgs& a, int sms, cudaStream_
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int sms, cudaStream_t st) {
-  const int grid = grid_for(a.tokens * a.cache.kv_heads * 2, 256 / (a.cache.dim >> 3), sms * 8);
-  if (a.bf16)
-    append_kernel<true><<<grid, 256, 0, st>>>(a);
+// A warp works on 128 / D pairs at a time.
+static int pair_grid(int64_t tokens, const Kv4Cache& c, int sms) {
+  return grid_for(tokens * c.kv_heads, 8 * (128 / c.dim), sms * 8);
+}
+
+template <int D>
+static void read_any(const Kv4ReadArgs& a, int grid, cudaStream_t st) {
+  if (a.out_dtype == WQ_F32)
+    read_kernel<D, WQ_F32><<<grid, 256, 0, st>>>(a);
+  else if (a.out_dtype == WQ_BF16)
+    read_kernel<D, WQ_BF16><<<grid, 256, 0, st>>>(a);
   else
-    append_kernel<false><<<grid, 256, 0, st>>>(a);
+    read_kernel<D, WQ_F16><<<grid, 256, 0, st>>>(a);
+}
+
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int sms, cudaStream_t st) {
+  const int grid = pair_grid(a.tokens, a.cache, sms);
+  if (a.cache.dim == 128) {
+    if (a.bf16) append_kernel<128, true><<<grid, 256, 0, st>>>(a);
+    else append_kernel<128, false><<<grid, 256, 0, st>>>(a);
+  } else {
+    if (a.bf16) append_kernel<64, true><<<grid, 256, 0, st>>>(a);
+    else append_kernel<64, false><<<grid, 256, 0, st>>>(a);
+  }
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_read(const Kv4ReadArgs& a, int sms, cudaStream_t st) {
-  const int grid = grid_for(a.tokens * a.cache.kv_heads * 2 * (a.cache.dim >> 3), 256, sms * 8);
-  if (a.out_dtype == WQ_F32)
-    read_kernel<WQ_F32><<<grid, 256, 0, st>>>(a);
-  else if (a.out_dtype == WQ_BF16)
-    read_kernel<WQ_BF16><<<grid, 256, 0, st>>>(a);
-  else
-    read_kernel<WQ_F16><<<grid, 256, 0, st>>>(a);
+  const int grid = pair_grid(a.tokens, a.cache, sms);
+  if (a.cache.dim == 128) read_any<128>(a, grid, st);
+  else read_any<64>(a, grid, st);
   return cudaGetLastError();
 }
 
