@@ -162,11 +162,11 @@ __device__ __forceinline__ float2 widen(uint32_t w) {
 // a half-integer on itself and leaves the others on their side. Adding 1.5 2^23 - 1536 + Ze, Ze
 // the zero-point rounded up to even, rounds to an integer with ties to even k; the low byte is
 // code + (Z & 1).
-__device__ __forceinline__ uint32_t encode8_snap(const float2 (&v)[4], const AsymScale& sz) {
-  const float z1 = static_cast<float>(static_cast<int>(sz.z) & 1);
+__device__ __forceinline__ uint32_t encode8_snap(const float2 (&v)[4], float inv_s, int z) {
+  const float z1 = static_cast<float>(z & 1);
   const float lo = 12582912.0f + z1, hi = lo + 15.0f;
-  const float2 inv2 = make_float2(sz.inv_s, sz.inv_s), g2 = make_float2(1536.0f, 1536.0f);
-  const float cz = 12581376.0f + (sz.z + z1);
+  const float2 inv2 = make_float2(inv_s, inv_s), g2 = make_float2(1536.0f, 1536.0f);
+  const float cz = 12581376.0f + (static_cast<float>(z) + z1);
   const float2 c2 = make_float2(cz, cz);
   uint32_t t[8];
 #pragma unroll
@@ -177,7 +177,7 @@ __device__ __forceinline__ uint32_t encode8_snap(const float2 (&v)[4], const Asy
   }
   const uint32_t ev = __byte_perm(__byte_perm(t[0], t[2], 0x0040), __byte_perm(t[4], t[6], 0x0040), 0x5410);
   const uint32_t od = __byte_perm(__byte_perm(t[1], t[3], 0x0040), __byte_perm(t[5], t[7], 0x0040), 0x5410);
-  return ev + (od << 4) - (static_cast<uint32_t>(sz.z) & 1u) * 0x11111111u;
+  return ev + (od << 4) - (z & 1u) * 0x11111111u;
 }
 
 // 4 x 4 bytes over the four lanes whose numbers differ in bits 1 and 2 only: lane j of them
@@ -227,16 +227,36 @@ struct Pairs {
   }
 };
 
+// Packed 16-bit minimum and maximum; a NaN propagates.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if (kBf16) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if (kBf16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // One lane holds 8 consecutive dimensions of a row (one 16-byte load, one 32-bit word of codes);
-// the group's range is reduced among its group/8 lanes by shuffles. S', Z and the codes are
-// decided exactly, as in quantize.cu. V's words are formed by a byte transpose among four lanes,
-// so that every store is a word. Bound by HBM: 2 B an element in, D/2 + 4 D/g bytes a row out.
-template <int D, bool kBf16>
-__global__ void __launch_bounds__(256) append_kernel(Kv4AppendArgs a) {
+// the group's range is reduced among its group/8 lanes by shuffles, in 16 bits. S', Z and the
+// codes are decided exactly, as in quantize.cu. A warp takes kRounds rounds of pairs at a time and
+// each lane decides S' and Z of one of their groups (the exact decision is half of a round's
+// instructions: 58 us for 16384 tokens of 8 heads of 128 with every lane deciding its own).
+// V's words are formed by a byte transpose among four lanes, so that every store is a word.
+// Bytes: 2 an element in, D/2 + 4 D/g a row out.
+template <int D, bool kBf16, int kRounds>
+__global__ void __launch_bounds__(256, 4) append_kernel(Kv4AppendArgs a) {
   using P = Pairs<D>;
   const Kv4Cache c = a.cache;
   const int lane = threadIdx.x & 31;
   const int glanes = c.group >> 3, groups = c.groups();
+  const int nseg = 32 / glanes;  // groups of a round
   const bool is_v = (lane / P::kLanes) & 1;
   const int w = lane % P::kLanes;
   const int64_t limit = c.num_blocks << c.block_log2;
@@ -245,49 +265,72 @@ __global__ void __launch_bounds__(256) append_kernel(Kv4AppendArgs a) {
   const uint16_t* base = (is_v ? a.V : a.K) + 8 * w;
   const int64_t s_tok = is_v ? a.v_tok : a.k_tok, s_head = is_v ? a.v_head : a.k_head;
   bool range = false, nonfinite = false;
-  // the trip count is the same for a whole warp: the shuffles need every lane
-  for (P p(c.kv_heads, lane); __any_sync(0xffffffffu, p.tok < a.tokens); p.next()) {
-    int slot = -1;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (p.tok < a.tokens) {
-      x = ld_stream_u4(base + p.tok * s_tok + p.head * s_head);
-      slot = __ldg(a.slots + p.tok);
-      if (slot >= limit) {
-        range = true;
-        slot = -1;
+  P p(c.kv_heads, lane);
+  while (__any_sync(0xffffffffu, p.tok < a.tokens)) {
+    uint4 x[kRounds];
+    int slot[kRounds], head[kRounds];
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+      x[u] = make_uint4(0, 0, 0, 0);
+      slot[u] = -1;
+      head[u] = p.head;
+      if (p.tok < a.tokens) {
+        x[u] = ld_stream_u4(base + p.tok * s_tok + p.head * s_head);
+        slot[u] = __ldg(a.slots + p.tok);
       }
+      p.next();
     }
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-    float2 v[4];
+    // the range of each round's groups; then this lane's group of all rounds
     float mn = 0.0f, mx = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = widen<kBf16>(xs[i]);
-      mn = fmin_nan(mn, fmin_nan(v[i].x, v[i].y));
-      mx = fmax_nan(mx, fmax_nan(v[i].x, v[i].y));
-    }
+    for (int u = 0; u < kRounds; ++u) {
+      uint32_t lo = min2<kBf16>(min2<kBf16>(x[u].x, x[u].y), min2<kBf16>(x[u].z, x[u].w));
+      uint32_t hi = max2<kBf16>(max2<kBf16>(x[u].x, x[u].y), max2<kBf16>(x[u].z, x[u].w));
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
-      if (o < glanes) {
-        mn = fmin_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      for (int o = 1; o < 16; o <<= 1) {
+        if (o < glanes) {
+          lo = min2<kBf16>(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = max2<kBf16>(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+      }
+      const int from = (lane % nseg) * glanes;
+      lo = __shfl_sync(0xffffffffu, lo, from);
+      hi = __shfl_sync(0xffffffffu, hi, from);
+      if (lane / nseg == u) {
+        const float2 l2 = widen<kBf16>(lo), h2 = widen<kBf16>(hi);
+        mn = fmin_nan(0.0f, fmin_nan(l2.x, l2.y));
+        mx = fmax_nan(0.0f, fmax_nan(h2.x, h2.y));
       }
     }
     const AsymScale sz = asym_scale_zero(mn, mx);
-    uint32_t word = sz.bad ? 0u : encode8_snap(v, sz);
-    const uint32_t turned = transpose_bytes(word, lane);
-    if (slot < 0) continue;
-    if (is_v) word = turned;
-    const int t = slot & (c.block - 1);
-    uint8_t* chunk = c.data + (static_cast<int64_t>(slot >> c.block_log2) * c.kv_heads + p.head) *
-                                  chunk_bytes;
-    *reinterpret_cast<uint32_t*>(chunk + (is_v ? codes : 0) + t * (D / 2) +
-                                 word_place<D>(is_v, w, t)) = word;
-    if (w % glanes == 0) {
-      uint32_t* szp = reinterpret_cast<uint32_t*>(chunk + 2 * codes) +
-                      (is_v ? c.block * groups : 0) + t * groups + w / glanes;
-      *szp = sz.sbits | f32_to_f16_bits(sz.z) << 16;
-      if (sz.bad) nonfinite = true;
+    const uint32_t mine = sz.bad ? 0x80003C00u : sz.sbits | static_cast<uint32_t>(sz.z) << 16;
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+      const int from = u * nseg + lane / glanes;
+      const uint32_t got = __shfl_sync(0xffffffffu, mine, from);
+      const float inv_s = __shfl_sync(0xffffffffu, sz.inv_s, from);
+      const bool bad = got >> 31;
+      const int z = (got >> 16) & 15;
+      const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      float2 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = widen<kBf16>(xs[i]);
+      uint32_t word = bad ? 0u : encode8_snap(v, inv_s, z);
+      const uint32_t turned = transpose_bytes(word, lane);
+      if (slot[u] >= limit) range = true;
+      if (slot[u] < 0 || slot[u] >= limit) continue;
+      if (is_v) word = turned;
+      const int t = slot[u] & (c.block - 1);
+      uint8_t* chunk = c.data + (static_cast<int64_t>(slot[u] >> c.block_log2) * c.kv_heads +
+                                 head[u]) * chunk_bytes;
+      *reinterpret_cast<uint32_t*>(chunk + (is_v ? codes : 0) + t * (D / 2) +
+                                   word_place<D>(is_v, w, t)) = word;
+      if (w % glanes == 0) {
+        uint32_t* szp = reinterpret_cast<uint32_t*>(chunk + 2 * codes) +
+                        (is_v ? c.block * groups : 0) + t * groups + w / glanes;
+        *szp = (got & 0xFFFFu) | f32_to_f16_bits(static_cast<float>(z)) << 16;
+        if (bad) nonfinite = true;
+      }
     }
   }
   if (range) set_status(a.status, kStRange);
@@ -308,23 +351,40 @@ __global__ void __launch_bounds__(256) read_kernel(Kv4ReadArgs a) {
   const int64_t codes = static_cast<int64_t>(c.block) * (D / 2);
   const int groups = c.groups(), my_group = 8 * w / c.group;
   bool range = false;
-  for (P p(c.kv_heads, lane); __any_sync(0xffffffffu, p.tok < a.tokens); p.next()) {
-    const bool in = p.tok < a.tokens;
-    int slot = in ? __ldg(a.slots + p.tok) : -1;
+  // two pairs ahead the slot, one ahead what is stored there
+  P p(c.kv_heads, lane), q1 = p, q2 = p;
+  int slot_next = -1;
+  uint32_t word_next = 0, sz_next = 0;
+  auto load_slot = [&]() { slot_next = q2.tok < a.tokens ? __ldg(a.slots + q2.tok) : -1; };
+  auto load_row = [&]() {
+    int slot = slot_next;
+    word_next = sz_next = 0;
     if (slot >= limit) {
       range = true;
       slot = -1;
     }
-    uint32_t word = 0, sz = 0;
     if (slot >= 0) {
       const int t = slot & (c.block - 1);
       const uint8_t* chunk =
-          c.data + (static_cast<int64_t>(slot >> c.block_log2) * c.kv_heads + p.head) * chunk_bytes;
-      word = __ldg(reinterpret_cast<const uint32_t*>(chunk + (is_v ? codes : 0) + t * (D / 2) +
-                                                     word_place<D>(is_v, w, t)));
-      sz = __ldg(reinterpret_cast<const uint32_t*>(chunk + 2 * codes) +
-                 (is_v ? c.block * groups : 0) + t * groups + my_group);
+          c.data + (static_cast<int64_t>(slot >> c.block_log2) * c.kv_heads + q1.head) * chunk_bytes;
+      word_next = __ldg(reinterpret_cast<const uint32_t*>(
+          chunk + (is_v ? codes : 0) + t * (D / 2) + word_place<D>(is_v, w, t)));
+      sz_next = __ldg(reinterpret_cast<const uint32_t*>(chunk + 2 * codes) +
+                      (is_v ? c.block * groups : 0) + t * groups + my_group);
     }
+  };
+  load_slot();
+  load_row();
+  q2.next();
+  load_slot();
+  for (; __any_sync(0xffffffffu, p.tok < a.tokens); p.next()) {
+    const bool in = p.tok < a.tokens;
+    uint32_t word = word_next;
+    const uint32_t sz = sz_next;
+    q1.next();
+    load_row();
+    q2.next();
+    load_slot();
     const uint32_t turned = transpose_bytes(word, lane);
     if (!in) continue;
     if (is_v) word = turned;
@@ -382,14 +442,26 @@ static void read_any(const Kv4ReadArgs& a, int grid, cudaStream_t st) {
     read_kernel<D, WQ_F16><<<grid, 256, 0, st>>>(a);
 }
 
-cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int sms, cudaStream_t st) {
+// Four rounds a warp where there are that many for all warps of the device (16384 tokens of 8
+// heads: 85 us with their read, 94 with one round), else one, for more warps at work (4099
+// tokens of 6 heads of 64: 19 us, 23 with four).
+template <int D, bool kBf16>
+static void append_any(const Kv4AppendArgs& a, int sms, cudaStream_t st) {
+  const int64_t per_round = static_cast<int64_t>(sms) * 4 * 8 * (128 / D);
   const int grid = pair_grid(a.tokens, a.cache, sms);
+  if (a.tokens * a.cache.kv_heads >= 4 * per_round)
+    append_kernel<D, kBf16, 4><<<grid, 256, 0, st>>>(a);
+  else
+    append_kernel<D, kBf16, 1><<<grid, 256, 0, st>>>(a);
+}
+
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int sms, cudaStream_t st) {
   if (a.cache.dim == 128) {
-    if (a.bf16) append_kernel<128, true><<<grid, 256, 0, st>>>(a);
-    else append_kernel<128, false><<<grid, 256, 0, st>>>(a);
+    if (a.bf16) append_any<128, true>(a, sms, st);
+    else append_any<128, false>(a, sms, st);
   } else {
-    if (a.bf16) append_kernel<64, true><<<grid, 256, 0, st>>>(a);
-    else append_kernel<64, false><<<grid, 256, 0, st>>>(a);
+    if (a.bf16) append_any<64, true>(a, sms, st);
+    else append_any<64, false>(a, sms, st);
   }
   return cudaGetLastError();
 }
