@@ -143,6 +143,30 @@ def test_append_and_read(dim, group, dtype, block, T, H):
             assert torch.equal(x.cpu(), torch.from_numpy(exact).float().to(out_dtype))
 
 
+@pytest.mark.parametrize("dim,group,dtype", [(128, 128, BF16), (128, 32, F16), (64, 64, F16), (64, 32, BF16)])
+def test_append_many_equals_append_in_pieces(dim, group, dtype):
+    """A call large enough for several rounds a warp stores what small calls do, tokens in any
+    order, some skipped, the last round ragged."""
+    T, H, block = 12345, 5 if dim == 128 else 11, 64
+    g = torch.Generator(device=DEV).manual_seed(dim + group)
+    k, v = (torch.randn(2, T, H, dim, generator=g, device=DEV) * 3).to(dtype).unbind(0)
+    slots = torch.randperm(T + 100, generator=g, device=DEV)[:T].int()
+    slots[::97] = -1
+    a = wq.wq_kv4_alloc(-(-(T + 100) // block), H, dim, group, block)
+    a.zero_()
+    b = a.clone()
+    wq.wq_kv4_append(k, v, slots, a, group=group)
+    for i in range(0, T, 500):
+        wq.wq_kv4_append(k[i: i + 500], v[i: i + 500], slots[i: i + 500], b, group=group)
+    ok()
+    assert torch.equal(a, b)
+    some = [1, 5000, T - 1]
+    got, _ = wq.wq_kv4_read(a, slots[some], dim, group=group)
+    q, s, z = quantized(k[some].double().cpu().numpy(), group)
+    exact = (s[..., None] * (q.reshape(3, H, -1, group) - z[..., None])).reshape(3, H, dim)
+    assert np.array_equal(got.double().cpu().numpy(), exact)
+
+
 def test_append_strided():
     """K and V as slices of a fused projection's output, heads in another order in memory."""
     T, H, D = 19, 4, 64
@@ -373,6 +397,54 @@ def test_long_context_split_over_the_grid():
     assert torch.equal(out, again), "deterministic"
 
 
+def dense(cache, table, kv, dim, group, block):
+    slots = table.long()[torch.arange(kv, device=DEV) // block] * block + torch.arange(kv, device=DEV) % block
+    return (x.double() for x in wq.wq_kv4_read(cache, slots.int(), dim, group=group))
+
+
+@pytest.mark.parametrize("dim,group,dtype", [(128, 128, BF16), (128, 128, F16), (128, 64, BF16), (128, 32, F16), (64, 64, BF16), (64, 32, F16)])
+@pytest.mark.parametrize("new,kv,heads,kv_heads,window", [(700, 3001, 4, 2, 0), (333, 2000, 7, 1, 900), (1, 9000, 24, 1, 0)])
+def test_long_prompts(dim, group, dtype, new, kv, heads, kv_heads, window):
+    """Many tiles of keys (every ring goes round several times), values whose scale grows a
+    thousandfold along the keys, against torch in float64."""
+    block = 32
+    g = torch.Generator(device=DEV).manual_seed(kv)
+    blocks = -(-kv // block)
+    cache = wq.wq_kv4_alloc(blocks, kv_heads, dim, group, block)
+    table = torch.randperm(blocks, generator=g, device=DEV).int()[None]
+    slots = table[0].long()[torch.arange(kv, device=DEV) // block] * block + torch.arange(kv, device=DEV) % block
+    k, v = torch.randn(2, kv, kv_heads, dim, generator=g, device=DEV).unbind(0)
+    v = v * torch.exp2(torch.linspace(-6, 4, kv, device=DEV))[:, None, None]
+    wq.wq_kv4_append(k.to(dtype), v.to(dtype), slots.int(), cache, group=group)
+    q = torch.randn(new, heads, dim, generator=g, device=DEV).to(dtype)
+    out, lse = wq.wq_kv4_attention(q, cache, table, ints([0, new]), ints([kv]), new, group=group, window=window, return_lse=True)
+    ok()
+    kk, vv = dense(cache, table[0], kv, dim, group, block)
+    s_max = 8 / 15  # of keys within 4 standard deviations to both sides
+    last = torch.arange(new, device=DEV)[:, None] + kv - new
+    hidden = torch.arange(kv, device=DEV) > last
+    if window:
+        hidden |= torch.arange(kv, device=DEV) <= last - window
+    for h in range(heads):
+        x = q[:, h].double()
+        s = (x @ kk[:, h * kv_heads // heads].T * dim**-0.5).masked_fill(hidden, -float("inf"))
+        p = torch.softmax(s, 1)
+        vh = vv[:, h * kv_heads // heads]
+        want = p @ vh
+        # the oracle's bound of a request, by rows
+        e = ((dim / 8 + 8) * 2.0**-23 * 31 * s_max + 2.0**-21) * dim**-0.5 * x.abs().sum(1)
+        rel = 2 * e + 2.0**-11 + 2.0**-20 + (kv / 16 + 64) * 2.0**-23
+        limit = rel[:, None] * (p @ vh.abs()) + (kv * 2.0**-31 + 2.0**-29) * 2.2 * vh.abs().max()
+        half_step = torch.finfo(dtype).eps / 2
+        limit = limit + (want.abs() + limit) * half_step
+        assert bool(((out[:, h].double() - want).abs() <= limit).all()), h
+        wl = torch.logsumexp(s, 1)
+        bound = e + 2.0**-20 * (1 + wl.abs()) + (kv / 16 + 64) * 2.0**-23
+        assert bool(((lse[:, h].double() - wl).abs() <= bound).all()), h
+    again = wq.wq_kv4_attention(q, cache, table, ints([0, new]), ints([kv]), new, group=group, window=window)
+    assert torch.equal(out, again), "deterministic"
+
+
 def test_bad_pages_and_lengths():
     """Table entries outside the cache and lengths beyond the table: reported, those keys left
     out, the rest right, other requests untouched."""
@@ -476,6 +548,48 @@ def test_graph_streams_and_workspaces():
     torch.cuda.synchronize()
     assert all(torch.equal(o, outs[0]) for o in outs)
     ok()
+
+
+def test_prompt_and_storage_in_a_graph():
+    """A whole step captured (tables, append, attention of a prompt and a single token) and
+    replayed with other lengths and contents."""
+    heads, kv_heads, dim, block = 8, 2, 64, 16
+    ctx, new = ints([0, 40]), ints([50, 1])
+    tables = torch.full((2, 8), -1, dtype=torch.int32, device=DEV)
+    tables[1, :3] = ints([20, 21, 22])
+    free = ints(np.arange(12))
+    cache = wq.wq_kv4_alloc(24, kv_heads, dim, dim, block)
+    cache.zero_()
+    x = torch.randn(64, 2, kv_heads, dim, device=DEV).to(F16)
+    q = torch.randn(64, heads, dim, device=DEV).to(F16)
+    out = torch.zeros_like(q)
+
+    def step():
+        slots, starts, kv, taken = wq.wq_kv4_block_tables(ctx, new, free, tables, block, 64)
+        wq.wq_kv4_append(x[:, 0], x[:, 1], slots, cache)
+        wq.wq_kv4_attention(q, cache, tables, starts, kv, 50, out=out)
+
+    keep = tables.clone()
+    step()
+    eager = out.clone()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step()
+    out.zero_(), cache.zero_(), tables.copy_(keep)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[:51], eager[:51]) and not bool(out[51:].any())
+    q.normal_(), x.normal_(), new.copy_(ints([3, 1])), out.zero_(), cache.zero_(), tables.copy_(keep)
+    g.replay()
+    torch.cuda.synchronize()
+    replayed = out.clone()
+    out.zero_(), cache.zero_(), tables.copy_(keep)
+    step()
+    ok()
+    assert torch.equal(replayed, out) and bool(out[:4].any()) and not bool(out[4:].any())
 
 
 def test_a_serving_run():
