@@ -403,9 +403,10 @@ def dense(cache, table, kv, dim, group, block):
 
 
 @pytest.mark.parametrize("dim,group,dtype", [(128, 128, BF16), (128, 128, F16), (128, 64, BF16), (128, 32, F16), (64, 64, BF16), (64, 32, F16)])
-@pytest.mark.parametrize("new,kv,heads,kv_heads,window", [(700, 3001, 4, 2, 0), (333, 2000, 7, 1, 900), (1, 9000, 24, 1, 0)])
+@pytest.mark.parametrize("new,kv,heads,kv_heads,window", [(700, 3001, 4, 2, 0), (333, 2000, 7, 1, 900), (1, 9000, 24, 1, 0), (300, 1500, 75, 75, 0)])
 def test_long_prompts(dim, group, dtype, new, kv, heads, kv_heads, window):
-    """Many tiles of keys (every ring goes round several times), values whose scale grows a
+    """Many tiles of keys (every ring goes round several times), split over CTAs and (75 heads)
+    not, values whose scale grows a
     thousandfold along the keys, against torch in float64."""
     block = 32
     g = torch.Generator(device=DEV).manual_seed(kv)

@@ -99,6 +99,7 @@ cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int max_q, int sms, cudaStre
 
 // Requests with more rows than a.most_rows, on tcgen05.
 constexpr int kKv4DecodeRows = 16;
-cudaError_t launch_kv4_prompt(const Kv4AttnArgs& a, cudaStream_t st);
+size_t kv4_prompt_workspace_bytes(int sms);
+cudaError_t launch_kv4_prompt(const Kv4AttnArgs& a, int sms, cudaStream_t st);
 
 }  // namespace wq

@@ -43,6 +43,12 @@ wq_status check_cache(const wq_kv4_cache* c, wq::Kv4Cache* k) {
   return WQ_OK;
 }
 
+// The prompt and the decode kernels of a call use it one after the other.
+size_t workspace_bytes(int sms) {
+  const size_t d = wq::kv4_decode_workspace_bytes(sms), p = wq::kv4_prompt_workspace_bytes(sms);
+  return d > p ? d : p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -133,7 +139,7 @@ size_t wq_kv4_attention_workspace_bytes(void) {
   int sms = 0;
   unsigned* status = nullptr;
   if (!wq::current_device(&sms, &status)) sms = 148;
-  return wq::kv4_decode_workspace_bytes(sms);
+  return workspace_bytes(sms);
 }
 
 wq_status wq_kv4_attention(const wq_kv4_attention_args* p, void* stream) {
@@ -163,7 +169,7 @@ wq_status wq_kv4_attention(const wq_kv4_attention_args* p, void* stream) {
   int sms = 0;
   unsigned* status = nullptr;
   if (!wq::current_device(&sms, &status)) return WQ_ERR_NODEVICE;
-  if (p->workspace_bytes < wq::kv4_decode_workspace_bytes(sms)) return WQ_ERR_SHAPE;
+  if (p->workspace_bytes < workspace_bytes(sms)) return WQ_ERR_SHAPE;
   if (!wq::pointers_on_current_device({p->Q, p->q_starts, p->kv_lens, p->tables, p->out, p->lse,
                                        p->workspace, c.data}))
     return WQ_ERR_DEVICE;
@@ -198,7 +204,7 @@ wq_status wq_kv4_attention(const wq_kv4_attention_args* p, void* stream) {
   a.most_rows = static_cast<int>(kIntMax);
   if (static_cast<int64_t>(p->max_q) * a.ratio > wq::kKv4DecodeRows) {
     a.most_rows = a.requests == 1 ? 0 : wq::kKv4DecodeRows;
-    const wq_status e = from_cuda(wq::launch_kv4_prompt(a, st));
+    const wq_status e = from_cuda(wq::launch_kv4_prompt(a, sms, st));
     if (e != WQ_OK || a.requests == 1) return e;
   }
   return from_cuda(wq::launch_kv4_decode(a, p->max_q, sms, st));

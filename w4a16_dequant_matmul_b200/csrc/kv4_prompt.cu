@@ -26,6 +26,10 @@
 // 3000 of a step's 5700 cycles). K and Q hold each eight dimensions in the order
 // 0 4 1 5 2 6 3 7, in which a word's codes come apart by shifts.
 //
+// Where the units are fewer than the SMs, as with a short chunk behind a long context, each is
+// split over its keys among several CTAs, which leave (O, m, l) in the workspace for a second
+// kernel to join in order.
+//
 // S_i and P_i share TMEM: S_i of the next keys is issued behind the product that reads P_i.
 // When the softmax of tile i wakes for S_i, that product has completed too (the same commit),
 // so it may touch O_i.
@@ -190,6 +194,17 @@ struct Unit {
   int t0, nt;              // first tile of 128 keys, number of tiles
 };
 
+// Workspace of split units: a descriptor per unit, then per CTA kRowsCta rows of D sums, m and l.
+struct JoinDesc {
+  int32_t parts;  // CTAs with a part; 0: no such unit, 1: already done
+  int32_t q0, rows, row0, head;
+  int32_t pad[3];
+};
+__host__ __device__ constexpr int64_t part_floats(int dim) {
+  return static_cast<int64_t>(kRowsCta) * (dim + 2);
+}
+constexpr int kLeastTiles = 4;  // tiles of a part, against the fixed cost of a CTA
+
 __device__ __forceinline__ void request_rows(const Kv4AttnArgs& a, int b, int& q0, int& qn) {
   int lo = a.q_starts[b], hi = a.q_starts[b + 1];
   lo = lo < 0 ? 0 : lo < a.tokens ? lo : a.tokens;
@@ -257,8 +272,12 @@ __device__ __forceinline__ float row_pass(uint32_t t_s, uint32_t vs, float k1, f
   return mx;
 }
 
-template <int D, int G, bool kBf16>
-__global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnArgs a) {
+// kJoin: units may be split. (A kernel of its own: with the choice at run time the loop of the
+// unsplit one was compiled 8 % slower.)
+template <int D, int G, bool kBf16, bool kJoin>
+__global__ void __launch_bounds__(kThreads, 1)
+kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
+  const int splits = kJoin ? splits_arg : 1;
   using C = Cfg<D, G, kBf16>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
@@ -293,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
 #pragma unroll
     for (int w = 0; w < 16; ++w)
       if (w < warp) incl += ctl->scan[w];
-    const int64_t want = blockIdx.x;
+    const int64_t want = blockIdx.x / splits;
     if (want >= incl - mine && want < incl) {
       int64_t off = want - (incl - mine);
       int b = static_cast<int>(r0);
@@ -330,18 +349,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
     }
     __syncthreads();
   }
-  if (ctl->b < 0) return;
-  if (warp == 12) {
-    tmem_alloc(&ctl->tmem_base, 512);
-    tmem_relinquish();
+  if (kJoin) pdl_launch_dependents();
+  const int split = kJoin ? blockIdx.x % splits : 0;
+  JoinDesc* desc = static_cast<JoinDesc*>(a.workspace) + blockIdx.x / splits;
+  if (ctl->b < 0) {
+    if (kJoin && split == 0 && threadIdx.x == 0) desc->parts = 0;
+    return;
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
 
   const int b = ctl->b, head = ctl->head;
   Unit u;
+  int parts = 1;
   {
     int qn;
     request_rows(a, b, u.q0, qn);
@@ -364,7 +382,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
     u.t0 = static_cast<int>(first / kN);
     const int64_t last_tile = (end + kN - 1) / kN;
     u.nt = last_tile > u.t0 ? static_cast<int>(last_tile - u.t0) : 1;
+    if (kJoin) {  // this CTA's share of the unit's tiles
+      parts = (u.nt + kLeastTiles - 1) / kLeastTiles;
+      if (parts > splits) parts = splits;
+      if (split == 0 && threadIdx.x == 0) *desc = {parts, u.q0, u.rows, u.row0, head, {0, 0, 0}};
+      if (split >= parts) return;
+      const int from = static_cast<int>(static_cast<int64_t>(u.nt) * split / parts);
+      u.nt = static_cast<int>(static_cast<int64_t>(u.nt) * (split + 1) / parts) - from;
+      u.t0 += from;
+    }
   }
+  if (warp == 12) {
+    tmem_alloc(&ctl->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
 
   if (warp < 8) {
     reg_inc<kRegsSoftmax>();
@@ -466,29 +501,49 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
     // --- the rows' results
     if (ok && wait_warp(&ctl->o_full, 0, ctl, a.status)) {
       tc_fence_after();
-      const float inv = l == 0.0f ? 0.0f : ex2(static_cast<float>(exponent)) / l;
-      uint16_t* dst = a.out + static_cast<int64_t>(u.q0 + tok) * a.o_tok +
-                      static_cast<int64_t>(h) * a.o_head;
+      if (kJoin && parts > 1) {
+        const float up = ex2(static_cast<float>(exponent));
+        float* dst = reinterpret_cast<float*>(static_cast<JoinDesc*>(a.workspace) +
+                                              gridDim.x / splits) +
+                     blockIdx.x * part_floats(D);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[32];
-        tmem_ld32(t_o + 32 * c, v);
-        tmem_wait_ld();
-        if (live) {
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(t_o + 32 * c, v);
+          tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t w[4];
+          for (int q = 0; q < 32; q += 4)
+            *reinterpret_cast<float4*>(dst + (i * kM + r) * D + 32 * c + q) =
+                make_float4(__uint_as_float(v[q]) * up, __uint_as_float(v[q + 1]) * up,
+                            __uint_as_float(v[q + 2]) * up, __uint_as_float(v[q + 3]) * up);
+        }
+        dst[kRowsCta * D + i * kM + r] = m;
+        dst[kRowsCta * (D + 1) + i * kM + r] = l;
+      } else {
+        const float inv = l == 0.0f ? 0.0f : ex2(static_cast<float>(exponent)) / l;
+        uint16_t* dst = a.out + static_cast<int64_t>(u.q0 + tok) * a.o_tok +
+                        static_cast<int64_t>(h) * a.o_head;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = narrow2<kBf16>(__uint_as_float(v[8 * q + 2 * e]) * inv,
-                                    __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
-            *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(t_o + 32 * c, v);
+          tmem_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = narrow2<kBf16>(__uint_as_float(v[8 * q + 2 * e]) * inv,
+                                      __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
         }
+        if (live && a.lse)
+          a.lse[static_cast<int64_t>(u.q0 + tok) * a.heads + h] =
+              l == 0.0f ? -INFINITY : (m - kLift + log2f(l)) * 0.6931471805599453f;
       }
-      if (live && a.lse)
-        a.lse[static_cast<int64_t>(u.q0 + tok) * a.heads + h] =
-            l == 0.0f ? -INFINITY : (m - kLift + log2f(l)) * 0.6931471805599453f;
     }
   } else if (warp < 12) {
     reg_dec<kRegsExpand>();
@@ -836,10 +891,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnAr
   }
 }
 
-template <int D, int G, bool kBf16>
-cudaError_t launch_t(const Kv4AttnArgs& a, int64_t units, cudaStream_t st) {
+// Rows of a split unit: out = sum_i O_i 2^(m_i - m) / l over its parts i, one warp a row.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4AttnArgs a, int units, int splits) {
+  pdl_wait();
+  const JoinDesc d = static_cast<const JoinDesc*>(a.workspace)[blockIdx.x];
+  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int rr = d.row0 + row;
+  if (d.parts <= 1 || rr >= d.rows) return;
+  constexpr int V = D / 32;
+  const float* base = reinterpret_cast<const float*>(
+                          static_cast<const JoinDesc*>(a.workspace) + units) +
+                      static_cast<int64_t>(blockIdx.x) * splits * part_floats(D);
+  float m = -INFINITY;
+  for (int i = lane; i < d.parts; i += 32)
+    m = fmaxf(m, base[i * part_floats(D) + kRowsCta * D + row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.0f, o[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) o[k] = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < d.parts; ++i) {
+    const float* p = base + i * part_floats(D);
+    const float x = p[kRowsCta * D + row];
+    const float f = x == -INFINITY ? 1.0f : ex2(x - m);  // O and l are 0 there, or NaN
+    l += f * p[kRowsCta * (D + 1) + row];
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(p + row * D + V * lane + k);
+      o[k] += f * v.x;
+      o[k + 1] += f * v.y;
+    }
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int tok = rr / a.ratio, h = d.head * a.ratio + rr - tok * a.ratio;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(d.q0 + tok) * a.o_tok +
+                                              static_cast<int64_t>(h) * a.o_head);
+#pragma unroll
+  for (int k = 0; k < V; k += 2) dst[(V * lane + k) >> 1] = narrow2<kBf16>(o[k] * inv, o[k + 1] * inv);
+  if (a.lse && lane == 0)
+    a.lse[static_cast<int64_t>(d.q0 + tok) * a.heads + h] =
+        l == 0.0f ? -INFINITY : (m - kLift + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int D, int G, bool kBf16, bool kJoin>
+cudaError_t launch_t(const Kv4AttnArgs& a, int64_t units, int splits, cudaStream_t st) {
   using C = Cfg<D, G, kBf16>;
-  auto kern = kv4_prompt_kernel<D, G, kBf16>;
+  auto kern = kv4_prompt_kernel<D, G, kBf16, kJoin>;
   static std::atomic<bool> attr[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -849,27 +948,50 @@ cudaError_t launch_t(const Kv4AttnArgs& a, int64_t units, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr[dev & 63].store(true, std::memory_order_release);
   }
-  kern<<<static_cast<unsigned>(units), kThreads, C::kSmem, st>>>(a);
-  return cudaGetLastError();
+  kern<<<static_cast<unsigned>(units * splits), kThreads, C::kSmem, st>>>(a, splits);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !kJoin) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units), kRowsCta / 8, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, kBf16>, a, static_cast<int>(units), splits);
 }
 
 template <int D, int G>
-cudaError_t launch_g(const Kv4AttnArgs& a, int64_t units, cudaStream_t st) {
-  return a.bf16 ? launch_t<D, G, true>(a, units, st) : launch_t<D, G, false>(a, units, st);
+cudaError_t launch_g(const Kv4AttnArgs& a, int64_t units, int splits, cudaStream_t st) {
+  if (splits > 1)
+    return a.bf16 ? launch_t<D, G, true, true>(a, units, splits, st)
+                  : launch_t<D, G, false, true>(a, units, splits, st);
+  return a.bf16 ? launch_t<D, G, true, false>(a, units, 1, st)
+                : launch_t<D, G, false, false>(a, units, 1, st);
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_prompt(const Kv4AttnArgs& a, cudaStream_t st) {
+size_t kv4_prompt_workspace_bytes(int sms) {
+  return static_cast<size_t>(sms) * (sizeof(JoinDesc) + part_floats(128) * sizeof(float));
+}
+
+cudaError_t launch_kv4_prompt(const Kv4AttnArgs& a, int sms, cudaStream_t st) {
   // an upper bound of the units: the lengths are on the device, CTAs without a unit return
   const int64_t units = (static_cast<int64_t>(a.tokens) * a.ratio / kRowsCta + a.requests) *
                         a.cache.kv_heads;
+  // (units splits <= sms, for which the workspace is made)
+  const int splits = units < sms ? static_cast<int>(sms / units) : 1;
   const int groups = a.cache.groups();
   if (a.cache.dim == 128) {
-    if (groups == 1) return launch_g<128, 1>(a, units, st);
-    return groups == 2 ? launch_g<128, 2>(a, units, st) : launch_g<128, 4>(a, units, st);
+    if (groups == 1) return launch_g<128, 1>(a, units, splits, st);
+    return groups == 2 ? launch_g<128, 2>(a, units, splits, st)
+                       : launch_g<128, 4>(a, units, splits, st);
   }
-  return groups == 1 ? launch_g<64, 1>(a, units, st) : launch_g<64, 2>(a, units, st);
+  return groups == 1 ? launch_g<64, 1>(a, units, splits, st)
+                     : launch_g<64, 2>(a, units, splits, st);
 }
 
 }  // namespace wq
