@@ -24,10 +24,11 @@
 // sums a unit's parts in CTA order, so results do not depend on timing.
 //
 // Data path. A producer warp streams each tile's blocks by bulk copies (one per block of a
-// head) through an mbarrier ring, and turns the scale words of the tile that it asked for three
-// tiles ago into the constants of the formulas above, once for all (each consumer lane did that
-// for itself at first: a tenth of all instructions); four warps take 32 tokens of every tile
-// each (two MMA blocks side by side: with one, a warp waited out the latency of every step), with their own softmax state, joined at the end of a unit.
+// head) through an mbarrier ring; four warps take 32 tokens of every tile each (two MMA blocks
+// side by side: with one, a warp waited out the latency of every step), with their own softmax
+// state, joined at the end of a unit. A lane turns the scale words of one of the warp's 32
+// tokens into the constants of the formulas above (every lane doing that for its own MMA rows,
+// four times over, was a tenth of all instructions; the producer doing it for all was late).
 #include <atomic>
 
 #include "common.cuh"
@@ -53,37 +54,13 @@ struct Cfg {
   // Constants of a token: k1[G], k2[G], lv, 1 / S_v, S_v,g / S_v (G > 1), padded to 16 bytes;
   // and a word of Z for its values (below).
   static constexpr int kRec = G == 1 ? 4 : G == 2 ? 8 : 16;
-  static constexpr int kConstBytes = kTile * 4 * (kRec + G);
+  static constexpr int kConstBytes = kTile * 4 * (kRec + G);  // 32 tokens of each warp
   static constexpr int kRows = 8 * NT;
   // by registers and shared memory
   static constexpr int kCtasPerSm = NT == 1 && (G == 1 || D == 64) ? 3 : 2;
-  static constexpr int kStages = D == 64 ? 4 : G == 1 && NT == 1 || G == 4 ? 3 : 4;
-  // Tiles from a copy's issue to the making of its constants. The copy waits for a tile kStages
-  // before it, so constants are ready kStages - 1 - kLag tiles ahead of their use.
-  static constexpr int kLag = kStages - 2;
+  static constexpr int kStages = D == 64 ? 4 : G == 1 && NT == 1 ? 3 : 4;
   static constexpr int kMergeFloats = 2 * kRows * (D + 1);  // two warps' O rows, padded
 };
-
-struct Ctl {
-  uint64_t full[8];   // a tile's bytes have landed
-  uint64_t ready[8];  // its constants are written
-  uint64_t empty[8];  // the consumers have read both
-  uint32_t pieces[8];  // bit i: piece i of the stage's tile is there
-  int32_t left[8];     // keys from the tile's first on
-  int64_t scan[kWarps + 1];
-  int64_t total;
-  int64_t off0;  // tiles of request b0 before this CTA's share
-  int b0;
-  volatile int abort;
-  float ml[kWarps][2][32];
-};
-
-template <int D, int G, int NT>
-constexpr int smem_bytes() {
-  using C = Cfg<D, G, NT>;
-  return C::kStages * (C::kStageBytes + C::kConstBytes) + C::kMergeFloats * 4 +
-         static_cast<int>(sizeof(Ctl));
-}
 
 // What one request asks of this kernel.
 struct Req {
@@ -93,6 +70,27 @@ struct Req {
     return static_cast<int64_t>(kv_heads) * row_tiles * (nt + kUnitCost);
   }
 };
+
+struct Ctl {
+  uint64_t full[8];   // a tile's bytes have landed
+  uint64_t empty[8];  // the consumers have read them
+  uint32_t pieces[8];  // bit i: piece i of the stage's tile is there
+  int32_t left[8];     // keys from the tile's first on
+  int64_t scan[kWarps + 1];
+  int64_t total;
+  int64_t off0;  // tiles of request b0 before this CTA's share
+  int b0;
+  Req r0;        // that request
+  volatile int abort;
+  float ml[kWarps][2][32];
+};
+
+template <int D, int G, int NT>
+constexpr int smem_bytes() {
+  using C = Cfg<D, G, NT>;
+  return C::kStages * C::kStageBytes + C::kConstBytes + C::kMergeFloats * 4 +
+         static_cast<int>(sizeof(Ctl));
+}
 
 template <int kRows>
 __device__ __forceinline__ Req request(const Kv4AttnArgs& a, int b) {
@@ -162,6 +160,9 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
@@ -213,7 +214,11 @@ struct Desc {
 constexpr int kMaxRows = 16;
 __host__ __device__ constexpr int part_floats(int dim) { return kMaxRows * (dim + 2); }
 
-__host__ __device__ inline int64_t share_begin(int64_t total, int live, int i) {
+// First place of share i of `live` equal ones (a 32-bit division where that suffices: the 64-bit
+// one is a subroutine).
+__device__ __forceinline__ int64_t share_begin(int64_t total, int live, int i) {
+  if (total < (1 << 21))  // live <= 2^11
+    return static_cast<uint32_t>(total) * static_cast<uint32_t>(i) / static_cast<uint32_t>(live);
   return total * i / live;
 }
 
@@ -227,7 +232,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   constexpr int VT = D / 16;  // 16-dim tiles of V: one byte of a lane's share each
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* consts = smem + kStages * C::kStageBytes;
-  float* merge = reinterpret_cast<float*>(consts + kStages * C::kConstBytes);
+  float* merge = reinterpret_cast<float*>(consts + C::kConstBytes);
   Ctl* ctl = reinterpret_cast<Ctl*>(merge + C::kMergeFloats);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -235,7 +240,6 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&ctl->full[s], 1);
-      mbar_init(&ctl->ready[s], 1);
       mbar_init(&ctl->empty[s], kWarps);
     }
     ctl->abort = 0;
@@ -278,8 +282,9 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
     if (begin < end && begin >= incl - mine && begin < incl) {  // one thread's requests hold it
       int64_t off = begin - (incl - mine);
       int b = static_cast<int>(r0);
+      Req r;
       while (true) {
-        const Req r = request<kRows>(a, b);
+        r = request<kRows>(a, b);
         const int64_t w = r.places(a.cache.kv_heads);
         if (off < w) break;
         off -= w;
@@ -287,6 +292,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
       }
       ctl->b0 = b;
       ctl->off0 = off;
+      ctl->r0 = r;
     }
     __syncthreads();
   }
@@ -304,15 +310,18 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
 
   // Position in the line: request, KV head, row tile, tile. The divisions are made once.
   int b = ctl->b0;
-  Req r = request<kRows>(a, b);
+  Req r = ctl->r0;
   int h, rt, t;
   int64_t left = end - begin;  // places from the tile's on
   int64_t line = begin;        // the unit's first place
   {
-    const int64_t unit = ctl->off0 / (r.nt + kUnitCost);
-    const int place = static_cast<int>(ctl->off0 - unit * (r.nt + kUnitCost));
-    h = static_cast<int>(unit / r.row_tiles);
-    rt = static_cast<int>(unit - static_cast<int64_t>(h) * r.row_tiles);
+    const int64_t off = ctl->off0;
+    const int each = r.nt + kUnitCost;
+    const int unit = off >> 32 ? static_cast<int>(off / each)  // < KV heads x row tiles
+                               : static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(each));
+    const int place = static_cast<int>(off - static_cast<int64_t>(unit) * each);
+    h = unit / r.row_tiles;
+    rt = unit - h * r.row_tiles;
     t = place - kUnitCost;
     line -= place;
     if (t < 0) {
@@ -339,68 +348,12 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
 
   if (warp == kWarps) {
     // ------------------------------------------------------------------ producer warp
-    uint32_t s = 0, phase = 0;    // ring position, and the parity of its fill
-    uint32_t cs = 0, cphase = 0;  // the same of the constants
+    uint32_t s = 0, phase = 0;  // ring position, and the parity of its fill
     uint32_t it = 0;
     int table_of = -1, first = 0, cached = -1;  // 32 pieces' blocks, read ahead by the lanes
     const int64_t chunk = kc.chunk_bytes();
     const int64_t codes = static_cast<int64_t>(kc.block) * (D / 2);
     const int64_t reach = static_cast<int64_t>(a.width) << kc.block_log2;
-    // (a stage's constants are free when its bytes are: the copy waited for that)
-    auto constants = [&]() -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&ctl->full[cs], cphase, kLimitNs) && !ctl->abort))
-        return false;
-      const uint32_t there = ctl->pieces[cs];
-      const int keys = ctl->left[cs];
-      const uint8_t* st = smem + cs * C::kStageBytes;
-      float* rec = reinterpret_cast<float*>(consts + cs * C::kConstBytes);
-      uint32_t* zrec = reinterpret_cast<uint32_t*>(rec + kTile * C::kRec);
-#pragma unroll
-      for (int q32 = 0; q32 < kTile / 32; ++q32) {
-        const int tok = lane + 32 * q32;
-        const int pc = tok >> piece_log2;
-        const bool in = tok < keys && ((there >> pc) & 1u);
-        const uint32_t* sz = reinterpret_cast<const uint32_t*>(st + pc * piece_bytes + piece * D) +
-                             (tok & (piece - 1)) * G;
-        float c[C::kRec];
-#pragma unroll
-        for (int i = 0; i < C::kRec; ++i) c[i] = 0.0f;
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-          const uint32_t ks = in ? sz[i] : 0u, vz = in ? sz[piece * G + i] : 0u;
-          const float sk = f16_bits_to_f32(ks & 0xFFFFu) * a.scale_log2;
-          c[i] = 16.0f * sk;
-          c[G + i] = sk * (16.0f + f16_bits_to_f32(ks >> 16));
-          const float sv = f16_bits_to_f32(vz & 0xFFFFu);
-          if (G > 1) c[2 * G + 2 + i] = sv;
-          top = fmaxf(top, sv);
-          // 1024 + Z (low) and -(64 + Z) as binary16: what the two nibbles of a byte are
-          // expanded with
-          const uint32_t z = vz >> 16;
-          zrec[tok * G + i] = (hfma2(z, 0x3C003C00u, 0x64006400u) & 0xFFFFu) |
-                              hfma2(z, 0xBC00BC00u, 0xD400D400u) << 16;
-        }
-        top = fmaxf(top, 5.9604644775390625e-8f);  // a cache of zeros: S = 0 counts as its value 0
-        c[2 * G] = in ? lg2(top) : -INFINITY;
-        c[2 * G + 1] = 1.0f / top;
-        if (G > 1) {
-#pragma unroll
-          for (int i = 0; i < G; ++i) c[2 * G + 2 + i] *= c[2 * G + 1];
-        }
-#pragma unroll
-        for (int q = 0; q < C::kRec; q += 4)
-          *reinterpret_cast<float4*>(rec + tok * C::kRec + q) =
-              make_float4(c[q], c[q + 1], c[q + 2], c[q + 3]);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->ready[cs]);
-      if (++cs == kStages) {
-        cs = 0;
-        cphase ^= 1u;
-      }
-      return true;
-    };
     bool ok = true;
     while (true) {
       const int tile = r.t0 + t;
@@ -455,14 +408,9 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
         s = 0;
         phase ^= 1u;
       }
-      if (it > C::kLag) {
-        ok = constants();
-        if (!ok) break;
-      }
       if (--left == 0) break;
       if (++t == r.nt && !next_unit()) break;
     }
-    for (uint32_t q = it > C::kLag ? it - C::kLag : 0; ok && q < it; ++q) ok = constants();
     if (!ok && lane == 0) {
       set_status(a.status, kStTimeout);
       ctl->abort = 1;
@@ -482,7 +430,8 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
   auto token_of = [](int rho) { return (rho & 8) + ((rho & 1) ? 4 + (((rho & 7) >> 1) ^ 3) : ((rho & 7) >> 1)); };
   const int tk0 = token_of(g);                        // K rows g (and + 8)
   const int tv0 = token_of(2 * c), tv1 = token_of(2 * c + 1);  // V slots (and + 8)
-  const uint32_t stage0 = smem_u32(smem), const0 = smem_u32(consts);
+  const uint32_t stage0 = smem_u32(smem);
+  const uint32_t ct = smem_u32(consts) + warp * 32 * 4 * (C::kRec + G);  // the warp's constants
   // the warp's two blocks of 16 tokens within a stage: their rows of K and of V
   uint32_t off_k[2], off_v[2];
 #pragma unroll
@@ -570,10 +519,50 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
           break;
         }
         const uint32_t st = stage0 + s * C::kStageBytes;
-        const uint32_t ct = const0 + s * C::kConstBytes;
         const int pos0 = (r.t0 + tl) * kTile + 32 * warp;  // first of the warp's 32 tokens
         // (tokens of them that do not exist have lv = -inf, and codes of some kind)
-        if (ctl->left[s] > 32 * warp) {
+        const int keys = ctl->left[s] - 32 * warp;
+        if (keys > 0) {
+          // -- constants of token `lane` of the warp's 32
+          {
+            const int tok = 32 * warp + lane;
+            const int pc = tok >> piece_log2;
+            const bool in = lane < keys && ((ctl->pieces[s] >> pc) & 1u);
+            const uint32_t sz = st + pc * piece_bytes + piece * D + (tok & (piece - 1)) * 4 * G;
+            float k[C::kRec];
+#pragma unroll
+            for (int i = 0; i < C::kRec; ++i) k[i] = 0.0f;
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+              const uint32_t ks = in ? lds32(sz + 4 * i) : 0u;
+              const uint32_t vz = in ? lds32(sz + (piece * G + i) * 4) : 0u;
+              const float sk = f16_bits_to_f32(ks & 0xFFFFu) * a.scale_log2;
+              k[i] = 16.0f * sk;
+              k[G + i] = sk * (16.0f + f16_bits_to_f32(ks >> 16));
+              const float sv = f16_bits_to_f32(vz & 0xFFFFu);
+              if (G > 1) k[G > 1 ? 2 * G + 2 + i : 0] = sv;
+              top = fmaxf(top, sv);
+              // 1024 + Z (low) and -(64 + Z) as binary16: what the two nibbles of a byte are
+              // expanded with
+              const uint32_t z = vz >> 16;
+              sts32(ct + (32 * C::kRec + lane * G + i) * 4,
+                    (hfma2(z, 0x3C003C00u, 0x64006400u) & 0xFFFFu) |
+                        hfma2(z, 0xBC00BC00u, 0xD400D400u) << 16);
+            }
+            top = fmaxf(top, 5.9604644775390625e-8f);  // a cache of zeros: S = 0 counts as its value 0
+            k[2 * G] = in ? lg2(top) : -INFINITY;
+            k[2 * G + 1] = __fdividef(1.0f, top);
+            if (G > 1) {
+#pragma unroll
+              for (int i = 0; i < G; ++i) k[G > 1 ? 2 * G + 2 + i : 0] *= k[2 * G + 1];
+            }
+#pragma unroll
+            for (int q = 0; q < C::kRec; q += 4)
+              sts128(ct + (lane * C::kRec + q) * 4,
+                     make_uint4(__float_as_uint(k[q]), __float_as_uint(k[q + 1]),
+                                __float_as_uint(k[q + 2]), __float_as_uint(k[q + 3])));
+          }
           // -- scores: two blocks of 16 tokens x 8 NT rows
           float d[2][NT][G][4];
 #pragma unroll
@@ -614,12 +603,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
               }
             }
           }
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(&ctl->ready[s], phase, kLimitNs))) {
-            set_status(a.status, kStTimeout);
-            ctl->abort = 1;
-            ok = false;
-            break;
-          }
+          __syncwarp();  // the constants are written
           // s = k1 D - k2 X + lv, in place of the block's D of group 0
           float isv[2][2], ratio[2][2][G];
           bool over = false;
@@ -632,7 +616,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
               const int tok = 16 * w + tk0 + 8 * e;
 #pragma unroll
               for (int q = 0; q < C::kRec; q += 4) {
-                const uint4 x = lds128(ct + ((32 * warp + tok) * C::kRec + q) * 4);
+                const uint4 x = lds128(ct + (tok * C::kRec + q) * 4);
                 k[q] = __uint_as_float(x.x);
                 k[q + 1] = __uint_as_float(x.y);
                 k[q + 2] = __uint_as_float(x.z);
@@ -715,14 +699,14 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
               }
             }
           uint32_t zlo[2][G][2], zhi[2][G][2];  // 1024 + Z and -(64 + Z) of the slot pairs
-          const uint32_t zt = ct + kTile * 4 * C::kRec;
+          const uint32_t zt = ct + 32 * 4 * C::kRec;
 #pragma unroll
           for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int i = 0; i < G; ++i)
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                const int tok = 32 * warp + 16 * w + 8 * q;
+                const int tok = 16 * w + 8 * q;
                 const uint32_t za = lds32(zt + ((tok + tv0) * G + i) * 4);
                 const uint32_t zb = lds32(zt + ((tok + tv1) * G + i) * 4);
                 zlo[w][i][q] = __byte_perm(za, zb, 0x5410);
