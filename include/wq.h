@@ -337,8 +337,9 @@ wq_status wq_kv4_read(const wq_kv4_cache* cache, const int32_t* slots, int64_t T
  *   lse = ln sum_j exp(scale q . k_j), [T, heads] float32, contiguous; may be NULL
  * A row that sees no key gives out = 0 and lse = -inf. Rows of Q outside q_starts are not
  * read, and their out and lse are left as they were. Scores, softmax statistics and sums are
- * fp32; probabilities are rounded once to binary16 (2^-12 relative) before they meet the
- * values, and out once to its type. The result is deterministic. max_q should be the largest
+ * fp32; probabilities are rounded once to binary16 (half a step, 2^-11) before they meet the
+ * values (which, where out is bf16 and a request has many rows, are too), and out once to its
+ * type. The result is deterministic. max_q should be the largest
  * number of rows of a request: it chooses kernels, and a wrong one costs time only.
  * Strides in elements, unit along head_dim, multiples of 8; Q, out, workspace 16-byte
  * aligned; Q and out bf16 or fp16. The workspace needs no initial contents; calls that may

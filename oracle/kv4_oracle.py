@@ -69,9 +69,8 @@ def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None):
     (`s_max`: the largest S of the request's keys); a binary16 part of S (q - Z) / 16 may be a
     subnormal, half a step of 2^-24 off. That makes every probability wrong by a relative
         e = ((D/8 + 8) 2^-23 31 S + 2^-21) scale sum|x|
-    at most, and numerator and denominator by e each; with it 2^-12 for its rounding to binary16
-    (half a step of 2^-11) and 2^-12 for that of its value, 2^-20 for exp2, log2 and the scale
-    products, and (kv/16 + 64) 2^-23 for the two fp32 sums over the keys. The error of out is
+    at most, and numerator and denominator by e each; with it 2^-11 for its rounding to binary16
+    (half a step) and 2^-11 for that of its value, 2^-20 for exp2, log2 and the scale products, and (kv/16 + 64) 2^-23 for the two fp32 sums over the keys. The error of out is
     that times sum_j p_j |v_j|. Where a rounded p is a binary16 subnormal it errs by half its
     step, 2^-25, with the largest p at 2^6 at least (or the largest p S, then a key's codes
     less Z are 15 at most): 2^-31 max|v| of every key, where 15 S <= 2.2 max_d |v_j| (the range
@@ -101,7 +100,7 @@ def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None):
             e = 0.0
             if s_max is not None:
                 e = ((dim / 8 + 8) * 2.0**-23 * 31 * s_max + 2.0**-21) * abs(scale) * np.abs(q[i, h]).sum()
-            rel = 2 * e + 2.0**-11 + 2.0**-20 + (kv / 16 + 64) * 2.0**-23
+            rel = 2 * e + 2.0**-10 + 2.0**-20 + (kv / 16 + 64) * 2.0**-23
             low = ((last + 1 - first) * 2.0**-31 / l + 2.0**-29) * 2.2 * np.abs(vv).max()
             bound[i, h] = rel * (p @ np.abs(vv) / l) + low
             bound_lse[i, h] = e + 2.0**-20 * (1 + abs(lse[i, h])) + (kv / 16 + 64) * 2.0**-23

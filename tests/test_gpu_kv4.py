@@ -388,9 +388,9 @@ def test_long_context_split_over_the_grid():
     s = torch.einsum("hd,kd->hk", q[0].double(), kk[:, 0].double()) * dim**-0.5
     p = torch.softmax(s, 1)
     want = p @ vv[:, 0].double()
-    # rounding of p 2^-12, of out 2^-8, sums and scores as in the oracle's bound (kv/16 steps)
+    # rounding of p 2^-11, of out 2^-8, sums and scores as in the oracle's bound (kv/16 steps)
     size = p @ vv[:, 0].double().abs()
-    limit = size * (2.0**-12 + 2.0**-14 + kv / 16 * 2.0**-23) + want.abs() * 2.0**-8
+    limit = size * (2.0**-11 + 2.0**-14 + kv / 16 * 2.0**-23) + want.abs() * 2.0**-8
     assert bool(((out[0].double() - want).abs() <= limit).all())
     assert torch.allclose(lse[0].double(), torch.logsumexp(s, 1), rtol=0, atol=1e-4)
     again = wq.wq_kv4_attention(q, cache, table, ints([0, 1]), ints([kv]), 1)
@@ -434,7 +434,7 @@ def test_long_prompts(dim, group, dtype, new, kv, heads, kv_heads, window):
         want = p @ vh
         # the oracle's bound of a request, by rows
         e = ((dim / 8 + 8) * 2.0**-23 * 31 * s_max + 2.0**-21) * dim**-0.5 * x.abs().sum(1)
-        rel = 2 * e + 2.0**-11 + 2.0**-20 + (kv / 16 + 64) * 2.0**-23
+        rel = 2 * e + 2.0**-10 + 2.0**-20 + (kv / 16 + 64) * 2.0**-23
         limit = rel[:, None] * (p @ vh.abs()) + (kv * 2.0**-31 + 2.0**-29) * 2.2 * vh.abs().max()
         half_step = torch.finfo(dtype).eps / 2
         limit = limit + (want.abs() + limit) * half_step

@@ -9,7 +9,7 @@
 // mma.sync m16n8k16 with 16 tokens as its rows and 8 query rows as its columns. The softmax is
 // taken in one pass with a running reference m. The value's scale joins the exponent:
 //     p = 2^(s + log2 S_v - m + 7),   l += p / S_v,   O += p (q_code - Z)
-// so p needs no range beyond its own and is rounded once to binary16 (2^-12 relative); the
+// so p needs no range beyond its own and is rounded once to binary16 (half a step, 2^-11); the
 // codes less Z are exact there, and O = sum p c / l. m moves only when a score passes it by
 // 2^8 (p <= 2^15 then); everything else is fp32. With several groups a row, S_v is the
 // largest of the token's and the others enter p as their ratio to it.
@@ -19,9 +19,10 @@
 // request balance alike, and the host needs no lengths. Each unit also has two empty places on
 // the line before its tiles, which is about what its beginning and end cost a CTA: without them,
 // CTAs with the short requests of a batch came in last (64 requests of up to 8192 keys: 108 us
-// with no, 99 / 98 / 100 with 1 / 2 / 3 places; 48 short ones of up to 3001: 62, 47 / 43 / 41). A share that covers a unit only in
-// part leaves (O, m, l) in the workspace, and a second kernel (programmatic dependent launch)
-// sums a unit's parts in CTA order, so results do not depend on timing.
+// with no, 99 / 98 / 100 with 1 / 2 / 3 places; 48 short ones of up to 3001: 62, 47 / 43 / 41).
+// A share that covers a unit only in part leaves (O, m, l) in the workspace, and a second kernel
+// (programmatic dependent launch) sums a unit's parts in CTA order, so results do not depend on
+// timing.
 //
 // Data path. A producer warp streams each tile's blocks by bulk copies (one per block of a
 // head) through an mbarrier ring; four warps take 32 tokens of every tile each (two MMA blocks
@@ -29,6 +30,13 @@
 // state, joined at the end of a unit. A lane turns the scale words of one of the warp's 32
 // tokens into the constants of the formulas above (every lane doing that for its own MMA rows,
 // four times over, was a tenth of all instructions; the producer doing it for all was late).
+//
+// Measured: one token over 131072 keys, 64 query and 8 KV heads of 128: 50 us, 2.9 TB/s (45 % of
+// a copy), 40 of it with no arithmetic at all: about 13 us are the launch, the search for the
+// share, the first copies and the joining kernel, and the copies alone run at 5.3 TB/s. A batch
+// of 64 such requests of up to 8192 keys in blocks of 16: 86 us, 3.3 TB/s. With the arithmetic
+// the ALU pipe is half busy (shifts, masks and byte permutes: 16 for 16 codes of K, 12 for 16 of
+// V) and 12 warps an SM do not hide all latencies.
 #include <atomic>
 
 #include "common.cuh"
