@@ -503,6 +503,31 @@ def test_a_wrong_max_q_changes_no_result():
     ok()
 
 
+def test_one_request_with_a_wrong_max_q():
+    for n in (1, 3, 90):
+        c = Case([300], [n], 8, 2, 64, 32, 32, F16, seed=n)
+        for max_q in (0, 1, 4000):
+            c.check(*c.run(max_q=max_q))
+    ok()
+
+
+def test_a_row_that_is_not_finite_stays_alone():
+    """NaN and infinity in one query row change no other row, of its tile or its request."""
+    for q_lens in ([1, 4], [60, 3]):
+        c = Case([200, 90], q_lens, 8, 2, 128, 128, 16, BF16, seed=7)
+        good, glse = c.run()
+        for bad in (float("nan"), float("inf")):
+            keep = c.q.clone()
+            c.q[0, 1] = bad
+            out, lse = c.run()
+            mask = torch.ones_like(glse, dtype=torch.bool)
+            mask[0, 1] = False
+            assert torch.equal(out[mask], good[mask]) and torch.equal(lse[mask], glse[mask])
+            assert bool(torch.isnan(out[0, 1]).all())
+            c.q = keep
+    ok()
+
+
 def test_many_requests():
     """More requests than threads of a CTA."""
     rng = np.random.default_rng(0)

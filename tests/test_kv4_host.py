@@ -83,7 +83,7 @@ def test_block_tables_checks(lib):
 
 
 def attention_args(**kw):
-    d = dict(Q=F, T=4, qt=512, qh=128, c=None, tab=F, w=4, ld=4, qs=F, kv=F, B=2, out=F, ot=512,
+    d = dict(Q=F, T=4, qt=512, qh=128, c=None, tab=F, w=4, ld=4, qs=F, kv=F, B=2, out=2 * F, ot=512,
              oh=128, lse=F, ws=F, wsb=1 << 40, dt=wq.WQ_BF16, heads=4, mq=2, causal=1, win=0,
              scale=0.1)
     d.update(kw)
@@ -102,7 +102,7 @@ def test_attention_checks(lib):
     assert f(T=0, Q=0) == OK and f(B=0, qs=0) == OK
     for bad in (dict(T=-1), dict(B=-1), dict(heads=0), dict(heads=3), dict(mq=-1), dict(win=-1),
                 dict(win=(1 << 30) + 1), dict(w=-1), dict(ld=3), dict(scale=float("inf")),
-                dict(scale=float("nan")), dict(qt=-8), dict(T=1 << 30)):
+                dict(scale=float("nan")), dict(qt=-8), dict(T=1 << 30), dict(B=65537)):
         assert f(**bad) == SHAPE, bad
     for bad in (dict(Q=0), dict(qs=0), dict(kv=0), dict(out=0), dict(ws=0), dict(tab=0),
                 dict(c=cache(data=0))):
@@ -111,7 +111,7 @@ def test_attention_checks(lib):
                 dict(qt=516), dict(qh=4), dict(ot=4), dict(oh=1)):
         assert f(**bad) == ALIGN, bad
     assert f(dt=wq.WQ_F32) == DTYPE
-    assert f(c=cache(dim=72)) == UNSUP
+    assert f(c=cache(dim=72)) == UNSUP and f(out=F) == UNSUP  # in place
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="host without a GPU only")
@@ -146,6 +146,57 @@ def test_binding_refuses():
         wq.wq_kv4_attention(x, c, ints(1, 4), ints(3), ints(2), 1, group=32)
     with pytest.raises(ValueError):
         wq.wq_kv4_block_tables(ints(2), ints(3), ints(4), ints(2, 4), 16, 8)
+
+
+def test_binding_makes_the_tensors_device_current(monkeypatch):
+    """A call on tensors of another device than the current one is made with theirs current, and
+    the current one is back afterwards (host-side stand-ins: no GPU is touched)."""
+    current, seen = [0], []
+
+    class Dev:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            self.prev, current[0] = current[0], self.d
+
+        def __exit__(self, *exc):
+            current[0] = self.prev
+
+    k = wq._kv4()
+    stub = type("Stub", (), dict(vars(k)))()
+    stub.device, stub.current_device = Dev, lambda: current[0]
+    stub.raw_stream = lambda d: 77
+    stub.empty = lambda shape, strides, dtype, device: torch.empty(shape, dtype=dtype)
+
+    def call(name):
+        def f(*args):
+            seen.append((name, current[0], args[-1]))
+            return 0
+        return f
+
+    for name in ("block_tables", "append", "read", "attention"):
+        setattr(stub, name, call(name))
+    stub.workspace_bytes = {1: 16}
+    monkeypatch.setattr(wq, "_KV4", stub)
+
+    class OnOne(torch.Tensor):
+        """A host tensor that says it is on device 1."""
+        def get_device(self):
+            return 1
+
+        device = property(lambda self: 1)
+
+    one = lambda t: t.as_subclass(OnOne)  # noqa: E731
+    ints = lambda *s: one(torch.zeros(s, dtype=torch.int32))  # noqa: E731
+    c = one(wq.wq_kv4_alloc(4, 2, 64, 32, 16, device="cpu"))
+    x = one(torch.zeros(3, 2, 64, dtype=torch.bfloat16))
+    wq.wq_kv4_append(x, x, ints(3), c, group=32)
+    wq.wq_kv4_read(c, ints(3), 64, group=32)
+    wq.wq_kv4_block_tables(ints(2), ints(2), ints(4), ints(2, 4), 16, 8)
+    wq.wq_kv4_attention(x, c, ints(1, 4), ints(2), ints(1), 3, group=32)
+    assert seen == [(n, 1, 77) for n in ("append", "read", "block_tables", "attention")]
+    assert current == [0]
 
 
 @pytest.mark.parametrize("dim", [64, 128])

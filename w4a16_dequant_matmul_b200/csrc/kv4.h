@@ -31,6 +31,9 @@ struct Kv4Cache {
   }
 };
 
+// Keys of a request that attention counts: positions are kept below 2^31 with room for a tile.
+constexpr int kKv4MaxKeys = 1 << 30;
+
 struct Kv4TablesArgs {
   const int32_t* ctx_lens;
   const int32_t* new_lens;

@@ -160,7 +160,8 @@ wq_status wq_kv4_attention(const wq_kv4_attention_args* p, void* stream) {
       p->o_head_stride < 0 || p->ld_tables < p->width)
     return WQ_ERR_SHAPE;
   // rows of a request are counted in 32 bits
-  if (!count_ok(p->B) || p->T > kIntMax / p->heads || !count_ok(p->width)) return WQ_ERR_SHAPE;
+  if (p->B > 65536 || p->T > kIntMax / p->heads || !count_ok(p->width)) return WQ_ERR_SHAPE;
+  if (p->Q == p->out) return WQ_ERR_UNSUPPORTED;  // CTAs that share a row read it at their own times
   if (!aligned(p->Q, 16) || !aligned(p->out, 16) || !aligned(p->lse, 4) ||
       !aligned(p->q_starts, 4) || !aligned(p->kv_lens, 4) || !aligned(p->tables, 4) ||
       !aligned(p->workspace, 16) || p->q_token_stride % 8 != 0 || p->q_head_stride % 8 != 0 ||

@@ -109,7 +109,7 @@ __device__ __forceinline__ Req request(const Kv4AttnArgs& a, int b) {
   const int kv = a.kv_lens[b];
   r.q0 = lo;
   r.qn = hi - lo;
-  r.kv = kv < 0 ? 0 : kv;
+  r.kv = kv < 0 ? 0 : kv < kKv4MaxKeys ? kv : kKv4MaxKeys;
   const int64_t rows = static_cast<int64_t>(r.qn) * a.ratio;
   r.row_tiles = rows > a.most_rows ? 0 : static_cast<int>((rows + kRows - 1) / kRows);
   int first = 0;
@@ -367,7 +367,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
       const int tile = r.t0 + t;
       const int p0 = tile << (kTileLog2 - piece_log2);  // first piece of the tile
       if (table_of != b || p0 < first || p0 + npieces > first + 32) {
-        if (table_of != b && r.kv > reach) set_status(a.status, kStRange);
+        if (table_of != b && (r.kv > reach || r.kv == kKv4MaxKeys)) set_status(a.status, kStRange);
         table_of = b;
         first = p0;
         const int64_t pos = static_cast<int64_t>(p0 + lane) << piece_log2;

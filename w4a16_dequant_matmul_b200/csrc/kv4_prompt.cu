@@ -371,7 +371,9 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
   {
     int qn;
     request_rows(a, b, u.q0, qn);
-    u.kv = a.kv_lens[b] < 0 ? 0 : a.kv_lens[b];
+    const int kv = a.kv_lens[b];
+    u.kv = kv < 0 ? 0 : kv < kKv4MaxKeys ? kv : kKv4MaxKeys;
+    if (u.kv == kKv4MaxKeys && threadIdx.x == 0) set_status(a.status, kStRange);
     u.rows = qn * a.ratio;
     u.row0 = ctl->tile * kRowsCta;
     u.shift = u.kv - qn;
