@@ -180,38 +180,73 @@ __device__ __forceinline__ uint32_t encode8_snap(const float2 (&v)[4], float inv
   return ev + (od << 4) - (z & 1u) * 0x11111111u;
 }
 
-// 4 x 4 bytes over the four lanes whose numbers differ in bits 1 and 2 only: lane j of them
-// (those two bits) gives up its bytes for byte j of each. Its own inverse.
-__device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane) {
-  uint32_t t = __shfl_xor_sync(0xffffffffu, w, 2);
-  w = __byte_perm(w, t, lane & 2 ? 0x3715 : 0x6240);
-  t = __shfl_xor_sync(0xffffffffu, w, 4);
-  return __byte_perm(w, t, lane & 4 ? 0x3276 : 0x5410);
+// How lanes share the rows of one kind (K or V) so that the stored order needs no exchange, or
+// one, between lanes: a lane's words (of 8 dimensions) are those that stand side by side in the
+// cache. K: lane c of 4 has the words 4 u + c, D/8 bytes at c D/8. V: lane h + 2 k of D/32 has the
+// words 2 (4 k + u) + h; a transpose of its 4 x 4 bytes gives for each byte column g = 4 h + b the
+// rows 4 k .. 4 k + 3. (One word a lane with its bytes moved by shuffles, four words stored apart:
+// 293 instructions for 256 elements of an append, 163 of a read, which bounded both.)
+template <int D, int G, bool kV>
+struct Share {
+  static constexpr int kLanes = kV ? D / 32 : 4;      // lanes of a row
+  static constexpr int kWords = D / 8 / kLanes;       // words of a lane
+  static constexpr int kRows = 32 / kLanes;           // rows of a warp
+  // groups of a lane, and the lanes that a group lies in, which hold the same groups
+  static constexpr int kGroups = kV ? (G >= 64 ? 1 : 2) : D / G;
+  static constexpr int kShared = kV ? (G == 128 ? 4 : 2) : 4;
+  static_assert(kWords % kGroups == 0 && kGroups <= kShared, "");
+  __device__ static int dim(int l, int u) {           // first dimension of lane l's word u
+    return kV ? 8 * (2 * (4 * (l >> 1) + u) + (l & 1)) : 8 * (4 * u + l);
+  }
+  __device__ static int first_group(int l) { return kV && G < 128 ? (l >> 1) * kGroups : 0; }
+};
+
+// 4 x 4 bytes: word i's byte b becomes word b's byte i. Its own inverse.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[0], w[1], 0x7362);
+  const uint32_t c = __byte_perm(w[2], w[3], 0x5140), d = __byte_perm(w[2], w[3], 0x7362);
+  w[0] = __byte_perm(a, c, 0x5410);
+  w[1] = __byte_perm(a, c, 0x7632);
+  w[2] = __byte_perm(b, d, 0x5410);
+  w[3] = __byte_perm(b, d, 0x7632);
 }
 
-// Byte offset within its row of the 32-bit word that lane w of a row's D/8 holds: of K, word w
-// of the dimensions' order (4 j + c is stored at c (D/32) + j); of V, after transpose_bytes,
-// byte column g = 4 (w & 1) + (w >> 1 & 3), rows 4 (w >> 3) .. + 3 (bytes 8 i + g of the
-// dimensions' order are stored at g (D/16) + i).
-template <int D>
-__device__ __forceinline__ int word_place(bool is_v, int w, int t) {
-  if (!is_v) return 4 * ((w & 3) * (D / 32) + (w >> 2));
-  const int at = (4 * (w & 1) + ((w >> 1) & 3)) * (D / 16) + 4 * (w >> 3);
-  return D == 128 && (t & 2) ? at ^ 32 : at;
+// A V row of 128: lane l and lane l ^ 2 hold the halves of the same byte columns 4 h + b in word
+// b; after join_halves lane l holds columns 4 h + 2 k and 4 h + 2 k + 1 whole, in two words each.
+__device__ __forceinline__ void join_halves(uint32_t (&w)[4], int l) {
+  const bool k = l & 2;
+  const uint32_t a = __shfl_xor_sync(0xffffffffu, k ? w[0] : w[2], 2);
+  const uint32_t b = __shfl_xor_sync(0xffffffffu, k ? w[1] : w[3], 2);
+  const uint32_t w1 = w[1];
+  w[0] = k ? a : w[0];
+  w[1] = k ? w[2] : a;
+  w[2] = k ? b : w1;
+  w[3] = k ? w[3] : b;
+}
+__device__ __forceinline__ void split_halves(uint32_t (&w)[4], int l) {
+  const bool k = l & 2;
+  const uint32_t a = __shfl_xor_sync(0xffffffffu, k ? w[0] : w[1], 2);
+  const uint32_t b = __shfl_xor_sync(0xffffffffu, k ? w[2] : w[3], 2);
+  const uint32_t w1 = w[1];
+  w[0] = k ? a : w[0];
+  w[1] = k ? b : w[2];
+  w[2] = k ? w1 : a;
+  w[3] = k ? w[3] : b;
 }
 
-// The (token, head) pairs that a warp's lanes work on: 128 / D of them at a time, the D/8 lanes
-// of a K row and of its V row side by side. Pairs are stepped through without divisions.
-template <int D>
-struct Pairs {
-  static constexpr int kLanes = D / 8, kPerWarp = 16 / kLanes;
+// Byte offset within a stored row of lane l's bytes.
+template <int D, bool kV>
+__device__ __forceinline__ int lane_place(int l, int t) {
+  if (!kV) return l * (D / 8);
+  if (D == 64) return 16 * l;
+  return (32 * (l & 1) + 8 * (l & 2)) ^ (t & 2 ? 32 : 0);
+}
+
+// Rows (token, head) in the order of the input, stepped through without divisions.
+struct Rows {
   int64_t tok, step_tok;
   int head, step_head, heads;
-  __device__ Pairs(int kv_heads, int lane) : heads(kv_heads) {
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-    const int64_t first = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) +
-                           (threadIdx.x >> 5)) * kPerWarp + lane / (2 * kLanes);
-    const int64_t step = warps * kPerWarp;
+  __device__ Rows(int kv_heads, int64_t first, int64_t step) : heads(kv_heads) {
     tok = first / heads;
     head = static_cast<int>(first - tok * heads);
     step_tok = step / heads;
@@ -243,176 +278,211 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// One lane holds 8 consecutive dimensions of a row (one 16-byte load, one 32-bit word of codes);
-// the group's range is reduced among its group/8 lanes by shuffles, in 16 bits. S', Z and the
-// codes are decided exactly, as in quantize.cu. A warp takes kRounds rounds of pairs at a time and
-// each lane decides S' and Z of one of their groups (the exact decision is half of a round's
-// instructions: 58 us for 16384 tokens of 8 heads of 128 with every lane deciding its own).
-// V's words are formed by a byte transpose among four lanes, so that every store is a word.
-// Bytes: 2 an element in, D/2 + 4 D/g a row out.
-template <int D, bool kBf16, int kRounds>
-__global__ void __launch_bounds__(256, 4) append_kernel(Kv4AppendArgs a) {
-  using P = Pairs<D>;
+// The group's range is reduced in 16 bits, in the lane first, then over the lanes that share it.
+// S', Z and the codes are decided exactly, as in quantize.cu; the lanes that share groups decide
+// one each and hand the results round.
+// Bytes: 2 an element in, D/2 + 4 D/g a row out: 16384 tokens of 8 heads of 128 in 23 us, 3.7
+// TB/s (50 us with a word a lane); two rows a lane with the decisions shared between them: 25.
+template <int D, int G, bool kBf16, bool kV>
+__device__ __forceinline__ void append_rows(const Kv4AppendArgs& a) {
+  using S = Share<D, G, kV>;
   const Kv4Cache c = a.cache;
-  const int lane = threadIdx.x & 31;
-  const int glanes = c.group >> 3, groups = c.groups();
-  const int nseg = 32 / glanes;  // groups of a round
-  const bool is_v = (lane / P::kLanes) & 1;
-  const int w = lane % P::kLanes;
+  const int lane = threadIdx.x & 31, l = lane % S::kLanes;
+  const int share = l % S::kShared, share0 = lane - share;
+  constexpr int kPer = S::kWords / S::kGroups;  // words of a group
   const int64_t limit = c.num_blocks << c.block_log2;
   const int64_t chunk_bytes = c.chunk_bytes();
-  const int64_t codes = static_cast<int64_t>(c.block) * (D / 2);
-  const uint16_t* base = (is_v ? a.V : a.K) + 8 * w;
-  const int64_t s_tok = is_v ? a.v_tok : a.k_tok, s_head = is_v ? a.v_head : a.k_head;
+  const int codes = c.block * (D / 2);
+  const uint16_t* base = kV ? a.V : a.K;
+  const int64_t s_tok = kV ? a.v_tok : a.k_tok, s_head = kV ? a.v_head : a.k_head;
   bool range = false, nonfinite = false;
-  P p(c.kv_heads, lane);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  Rows p(c.kv_heads, warp * S::kRows + lane / S::kLanes, warps * S::kRows);
   while (__any_sync(0xffffffffu, p.tok < a.tokens)) {
-    uint4 x[kRounds];
-    int slot[kRounds], head[kRounds];
+    const bool in = p.tok < a.tokens;
+    const int head = p.head;
+    const uint16_t* row = base + (in ? p.tok * s_tok + p.head * s_head : 0) + S::dim(l, 0);
+    uint4 x[S::kWords];
 #pragma unroll
-    for (int u = 0; u < kRounds; ++u) {
-      x[u] = make_uint4(0, 0, 0, 0);
-      slot[u] = -1;
-      head[u] = p.head;
-      if (p.tok < a.tokens) {
-        x[u] = ld_stream_u4(base + p.tok * s_tok + p.head * s_head);
-        slot[u] = __ldg(a.slots + p.tok);
+    for (int u = 0; u < S::kWords; ++u)
+      x[u] = in ? ld_stream_u4(row + (S::dim(0, u) - S::dim(0, 0))) : make_uint4(0, 0, 0, 0);
+    const int slot = in ? __ldg(a.slots + p.tok) : -1;
+    p.next();
+    uint32_t mn = 0, mx = 0;  // the range of this lane's group
+#pragma unroll
+    for (int g = 0; g < S::kGroups; ++g) {
+      uint32_t lo = x[g * kPer].x, hi = lo;
+#pragma unroll
+      for (int u = g * kPer; u < (g + 1) * kPer; ++u) {
+        lo = min2<kBf16>(min2<kBf16>(lo, x[u].x), min2<kBf16>(min2<kBf16>(x[u].y, x[u].z), x[u].w));
+        hi = max2<kBf16>(max2<kBf16>(hi, x[u].x), max2<kBf16>(max2<kBf16>(x[u].y, x[u].z), x[u].w));
       }
-      p.next();
+#pragma unroll
+      for (int o = 1; o < S::kShared; o <<= 1) {
+        lo = min2<kBf16>(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max2<kBf16>(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+      const bool own = share % S::kGroups == g;
+      mn = own ? lo : mn;
+      mx = own ? hi : mx;
     }
-    // the range of each round's groups; then this lane's group of all rounds
-    float mn = 0.0f, mx = 0.0f;
-#pragma unroll
-    for (int u = 0; u < kRounds; ++u) {
-      uint32_t lo = min2<kBf16>(min2<kBf16>(x[u].x, x[u].y), min2<kBf16>(x[u].z, x[u].w));
-      uint32_t hi = max2<kBf16>(max2<kBf16>(x[u].x, x[u].y), max2<kBf16>(x[u].z, x[u].w));
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) {
-        if (o < glanes) {
-          lo = min2<kBf16>(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-          hi = max2<kBf16>(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-      }
-      const int from = (lane % nseg) * glanes;
-      lo = __shfl_sync(0xffffffffu, lo, from);
-      hi = __shfl_sync(0xffffffffu, hi, from);
-      if (lane / nseg == u) {
-        const float2 l2 = widen<kBf16>(lo), h2 = widen<kBf16>(hi);
-        mn = fmin_nan(0.0f, fmin_nan(l2.x, l2.y));
-        mx = fmax_nan(0.0f, fmax_nan(h2.x, h2.y));
-      }
-    }
-    const AsymScale sz = asym_scale_zero(mn, mx);
+    const float2 l2 = widen<kBf16>(mn), h2 = widen<kBf16>(mx);
+    const AsymScale sz = asym_scale_zero(fmin_nan(0.0f, fmin_nan(l2.x, l2.y)),
+                                         fmax_nan(0.0f, fmax_nan(h2.x, h2.y)));
     const uint32_t mine = sz.bad ? 0x80003C00u : sz.sbits | static_cast<uint32_t>(sz.z) << 16;
+    uint32_t word[S::kWords], got = mine;
+    float inv_s = sz.inv_s;
 #pragma unroll
-    for (int u = 0; u < kRounds; ++u) {
-      const int from = u * nseg + lane / glanes;
-      const uint32_t got = __shfl_sync(0xffffffffu, mine, from);
-      const float inv_s = __shfl_sync(0xffffffffu, sz.inv_s, from);
-      const bool bad = got >> 31;
-      const int z = (got >> 16) & 15;
-      const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float2 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = widen<kBf16>(xs[i]);
-      uint32_t word = bad ? 0u : encode8_snap(v, inv_s, z);
-      const uint32_t turned = transpose_bytes(word, lane);
-      if (slot[u] >= limit) range = true;
-      if (slot[u] < 0 || slot[u] >= limit) continue;
-      if (is_v) word = turned;
-      const int t = slot[u] & (c.block - 1);
-      uint8_t* chunk = c.data + (static_cast<int64_t>(slot[u] >> c.block_log2) * c.kv_heads +
-                                 head[u]) * chunk_bytes;
-      *reinterpret_cast<uint32_t*>(chunk + (is_v ? codes : 0) + t * (D / 2) +
-                                   word_place<D>(is_v, w, t)) = word;
-      if (w % glanes == 0) {
-        uint32_t* szp = reinterpret_cast<uint32_t*>(chunk + 2 * codes) +
-                        (is_v ? c.block * groups : 0) + t * groups + w / glanes;
-        *szp = (got & 0xFFFFu) | f32_to_f16_bits(static_cast<float>(z)) << 16;
-        if (bad) nonfinite = true;
+    for (int u = 0; u < S::kWords; ++u) {
+      if (S::kGroups > 1 && u % kPer == 0) {
+        got = __shfl_sync(0xffffffffu, mine, share0 + u / kPer);
+        inv_s = __shfl_sync(0xffffffffu, sz.inv_s, share0 + u / kPer);
       }
+      const float2 f[4] = {widen<kBf16>(x[u].x), widen<kBf16>(x[u].y), widen<kBf16>(x[u].z),
+                           widen<kBf16>(x[u].w)};
+      word[u] = got >> 31 ? 0u : encode8_snap(f, inv_s, (got >> 16) & 15);
+    }
+    if constexpr (kV) {
+      transpose4(word);
+      if (D == 128) join_halves(word, l);
+    }
+    if (slot >= limit) range = true;
+    if (slot < 0 || slot >= limit) continue;
+    const int t = slot & (c.block - 1);
+    uint8_t* chunk = c.data +
+        (static_cast<int64_t>(slot >> c.block_log2) * c.kv_heads + head) * chunk_bytes;
+    uint8_t* dst = chunk + (kV ? codes : 0) + t * (D / 2) + lane_place<D, kV>(l, t);
+    if constexpr (S::kWords == 4)
+      *reinterpret_cast<uint4*>(dst) = make_uint4(word[0], word[1], word[2], word[3]);
+    else
+      *reinterpret_cast<uint2*>(dst) = make_uint2(word[0], word[1]);
+    if (share < S::kGroups) {
+      reinterpret_cast<uint32_t*>(chunk + 2 * codes)[((kV ? c.block : 0) + t) * (D / G) +
+                                                     S::first_group(l) + share] =
+          (mine & 0xFFFFu) | f32_to_f16_bits(static_cast<float>((mine >> 16) & 15)) << 16;
+      if (sz.bad) nonfinite = true;
     }
   }
   if (range) set_status(a.status, kStRange);
   if (nonfinite) set_status(a.status, kStNonFinite);
 }
 
-// The inverse: one lane gives 8 consecutive values S'(q - Z) of a row (exact in fp32, or
-// rounded once to 16 bits); slot < 0 gives zeros. Bound by HBM: the values written.
-template <int D, int kOut>  // kOut: WQ_F32, WQ_BF16, WQ_F16
-__global__ void __launch_bounds__(256) read_kernel(Kv4ReadArgs a) {
-  using P = Pairs<D>;
+// CTAs of 4 warps; at most 16 of a kind for each SM, then each goes on to further rows (65536
+// tokens of 8 heads of 128, append and fp32 read: 74 and 106 us; with 8: 78 and 128; with 4: 81
+// and 112).
+constexpr int kRowThreads = 128, kRowCtas = 16;
+
+// blockIdx.y: 0 the keys, 1 the values.
+template <int D, int G, bool kBf16>
+__global__ void __launch_bounds__(kRowThreads) append_kernel(Kv4AppendArgs a) {
+  if (blockIdx.y == 0) append_rows<D, G, kBf16, false>(a);
+  else append_rows<D, G, kBf16, true>(a);
+}
+
+// The inverse, with the lanes and words of the append: values S'(q - Z), exact in fp32, or
+// rounded once to 16 bits; slot < 0 gives zeros. The slots of the next rows are loaded ahead.
+// Bound by HBM: 16384 tokens of 8 heads of 128 to fp32 in 29 us, 5.2 TB/s (39 us with a word a
+// lane; 51 us where each lane stores its own 32 bytes in two halves), to 16 bits in 17 us.
+template <int D, int G, int kOut, bool kV>  // kOut: WQ_F32, WQ_BF16, WQ_F16
+__device__ __forceinline__ void read_rows(const Kv4ReadArgs& a) {
+  using S = Share<D, G, kV>;
   const Kv4Cache c = a.cache;
-  const int lane = threadIdx.x & 31;
-  const bool is_v = (lane / P::kLanes) & 1;
-  const int w = lane % P::kLanes;
+  const int lane = threadIdx.x & 31, l = lane % S::kLanes;
   const int64_t limit = c.num_blocks << c.block_log2;
   const int64_t chunk_bytes = c.chunk_bytes();
-  const int64_t codes = static_cast<int64_t>(c.block) * (D / 2);
-  const int groups = c.groups(), my_group = 8 * w / c.group;
+  const int codes = c.block * (D / 2);
   bool range = false;
-  // two pairs ahead the slot, one ahead what is stored there
-  P p(c.kv_heads, lane), q1 = p, q2 = p;
-  int slot_next = -1;
-  uint32_t word_next = 0, sz_next = 0;
-  auto load_slot = [&]() { slot_next = q2.tok < a.tokens ? __ldg(a.slots + q2.tok) : -1; };
-  auto load_row = [&]() {
-    int slot = slot_next;
-    word_next = sz_next = 0;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  Rows p(c.kv_heads, warp * S::kRows + lane / S::kLanes, warps * S::kRows);
+  int next = p.tok < a.tokens ? __ldg(a.slots + p.tok) : -1;
+  while (__any_sync(0xffffffffu, p.tok < a.tokens)) {
+    const bool in = p.tok < a.tokens;
+    const int64_t row = p.tok * c.kv_heads + p.head;
+    const int head = p.head;
+    int slot = next;
+    p.next();
+    next = p.tok < a.tokens ? __ldg(a.slots + p.tok) : -1;
     if (slot >= limit) {
       range = true;
       slot = -1;
     }
+    uint32_t word[S::kWords], sz[S::kGroups];
+#pragma unroll
+    for (int u = 0; u < S::kWords; ++u) word[u] = 0;
+#pragma unroll
+    for (int g = 0; g < S::kGroups; ++g) sz[g] = 0;
     if (slot >= 0) {
       const int t = slot & (c.block - 1);
       const uint8_t* chunk =
-          c.data + (static_cast<int64_t>(slot >> c.block_log2) * c.kv_heads + q1.head) * chunk_bytes;
-      word_next = __ldg(reinterpret_cast<const uint32_t*>(
-          chunk + (is_v ? codes : 0) + t * (D / 2) + word_place<D>(is_v, w, t)));
-      sz_next = __ldg(reinterpret_cast<const uint32_t*>(chunk + 2 * codes) +
-                      (is_v ? c.block * groups : 0) + t * groups + my_group);
-    }
-  };
-  load_slot();
-  load_row();
-  q2.next();
-  load_slot();
-  for (; __any_sync(0xffffffffu, p.tok < a.tokens); p.next()) {
-    const bool in = p.tok < a.tokens;
-    uint32_t word = word_next;
-    const uint32_t sz = sz_next;
-    q1.next();
-    load_row();
-    q2.next();
-    load_slot();
-    const uint32_t turned = transpose_bytes(word, lane);
-    if (!in) continue;
-    if (is_v) word = turned;
-    const float s = f16_bits_to_f32(sz & 0xFFFFu), z = f16_bits_to_f32(sz >> 16);
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = s * (static_cast<float>((word >> (4 * j)) & 15u) - z);
-    const int64_t at = (p.tok * c.kv_heads + p.head) * D + 8 * w;
-    if (kOut == WQ_F32) {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(is_v ? a.V : a.K) + at);
-      dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-      dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (kOut == WQ_BF16) {
-          o[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-        } else {
-          const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-          o[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+          c.data + (static_cast<int64_t>(slot >> c.block_log2) * c.kv_heads + head) * chunk_bytes;
+      const uint8_t* src = chunk + (kV ? codes : 0) + t * (D / 2) + lane_place<D, kV>(l, t);
+      if constexpr (S::kWords == 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+        word[0] = v.x, word[1] = v.y, word[2] = v.z, word[3] = v.w;
+      } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+        word[0] = v.x, word[1] = v.y;
       }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? a.V : a.K) + at) =
-          make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+      for (int g = 0; g < S::kGroups; ++g)
+        sz[g] = __ldg(reinterpret_cast<const uint32_t*>(chunk + 2 * codes) +
+                      ((kV ? c.block : 0) + t) * (D / G) + S::first_group(l) + g);
+    }
+    if constexpr (kV) {
+      if (D == 128) split_halves(word, l);
+      transpose4(word);
+    }
+#pragma unroll
+    for (int u = 0; u < S::kWords; ++u) {
+      const uint32_t g = sz[u / (S::kWords / S::kGroups)];
+      const float s = f16_bits_to_f32(g & 0xFFFFu);
+      // q - Z as (2^23 + q) - (2^23 + Z), exact
+      const float z = -(8388608.0f + f16_bits_to_f32(g >> 16));
+      const uint32_t ev = word[u] & 0x0F0F0F0Fu, od = (word[u] >> 4) & 0x0F0F0F0Fu;
+      auto value2 = [&](uint32_t e, uint32_t o, int j) {  // of bytes j of e and o
+        const float2 q = make_float2(__uint_as_float(__byte_perm(e, 0x4B000000u, 0x7650 + j)),
+                                     __uint_as_float(__byte_perm(o, 0x4B000000u, 0x7650 + j)));
+        return __fmul2_rn(__fadd2_rn(q, make_float2(z, z)), make_float2(s, s));
+      };
+      if (kOut == WQ_F32) {
+        // two neighbours (of one group) write 32 bytes of one's word, then of the other's
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t n = __shfl_sync(0xffffffffu, word[u], (lane & ~1) + i) >> (16 * (l & 1));
+          const float2 v0 = value2(n & 0x0F0Fu, (n >> 4) & 0x0F0Fu, 0);
+          const float2 v1 = value2(n & 0x0F0Fu, (n >> 4) & 0x0F0Fu, 1);
+          if (in)
+            *reinterpret_cast<float4*>(static_cast<float*>(kV ? a.V : a.K) + row * D +
+                                       S::dim((l & ~1) + i, u) + 4 * (l & 1)) =
+                make_float4(v0.x, v0.y, v1.x, v1.y);
+        }
+      } else {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 v = value2(ev, od, j);
+          if (kOut == WQ_BF16) {
+            o[j] = pack_bf16x2(v.x, v.y);
+          } else {
+            const __half2 h = __floats2half2_rn(v.x, v.y);
+            o[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        if (in)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kV ? a.V : a.K) + row * D +
+                                    S::dim(l, u)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
   if (range) set_status(a.status, kStRange);
+}
+
+template <int D, int G, int kOut>
+__global__ void __launch_bounds__(kRowThreads) read_kernel(Kv4ReadArgs a) {
+  if (blockIdx.y == 0) read_rows<D, G, kOut, false>(a);
+  else read_rows<D, G, kOut, true>(a);
 }
 
 int grid_for(int64_t items, int per_cta, int cap) {
@@ -427,49 +497,52 @@ cudaError_t launch_kv4_block_tables(const Kv4TablesArgs& a, int sms, cudaStream_
   return cudaGetLastError();
 }
 
-// A warp works on 128 / D pairs at a time.
-static int pair_grid(int64_t tokens, const Kv4Cache& c, int sms) {
-  return grid_for(tokens * c.kv_heads, 8 * (128 / c.dim), sms * 8);
+// CTAs of each kind for tokens x heads rows, 8 (of V, D = 64: 16) a warp.
+static dim3 row_grid(int64_t tokens, const Kv4Cache& c, int sms) {
+  return dim3(grid_for(tokens * c.kv_heads, 8 * (kRowThreads / 32), sms * kRowCtas), 2);
 }
 
-template <int D>
-static void read_any(const Kv4ReadArgs& a, int grid, cudaStream_t st) {
+template <int D, int G>
+static void read_any(const Kv4ReadArgs& a, dim3 grid, cudaStream_t st) {
   if (a.out_dtype == WQ_F32)
-    read_kernel<D, WQ_F32><<<grid, 256, 0, st>>>(a);
+    read_kernel<D, G, WQ_F32><<<grid, kRowThreads, 0, st>>>(a);
   else if (a.out_dtype == WQ_BF16)
-    read_kernel<D, WQ_BF16><<<grid, 256, 0, st>>>(a);
+    read_kernel<D, G, WQ_BF16><<<grid, kRowThreads, 0, st>>>(a);
   else
-    read_kernel<D, WQ_F16><<<grid, 256, 0, st>>>(a);
+    read_kernel<D, G, WQ_F16><<<grid, kRowThreads, 0, st>>>(a);
 }
 
-// Four rounds a warp where there are that many for all warps of the device (16384 tokens of 8
-// heads: 85 us with their read, 94 with one round), else one, for more warps at work (4099
-// tokens of 6 heads of 64: 19 us, 23 with four).
-template <int D, bool kBf16>
-static void append_any(const Kv4AppendArgs& a, int sms, cudaStream_t st) {
-  const int64_t per_round = static_cast<int64_t>(sms) * 4 * 8 * (128 / D);
-  const int grid = pair_grid(a.tokens, a.cache, sms);
-  if (a.tokens * a.cache.kv_heads >= 4 * per_round)
-    append_kernel<D, kBf16, 4><<<grid, 256, 0, st>>>(a);
-  else
-    append_kernel<D, kBf16, 1><<<grid, 256, 0, st>>>(a);
+template <int D, int G>
+static void append_any(const Kv4AppendArgs& a, dim3 grid, cudaStream_t st) {
+  if (a.bf16) append_kernel<D, G, true><<<grid, kRowThreads, 0, st>>>(a);
+  else append_kernel<D, G, false><<<grid, kRowThreads, 0, st>>>(a);
 }
 
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int sms, cudaStream_t st) {
-  if (a.cache.dim == 128) {
-    if (a.bf16) append_any<128, true>(a, sms, st);
-    else append_any<128, false>(a, sms, st);
+  const Kv4Cache& c = a.cache;
+  const dim3 grid = row_grid(a.tokens, c, sms);
+  if (c.dim == 64) {
+    if (c.group == 32) append_any<64, 32>(a, grid, st);
+    else append_any<64, 64>(a, grid, st);
   } else {
-    if (a.bf16) append_any<64, true>(a, sms, st);
-    else append_any<64, false>(a, sms, st);
+    if (c.group == 32) append_any<128, 32>(a, grid, st);
+    else if (c.group == 64) append_any<128, 64>(a, grid, st);
+    else append_any<128, 128>(a, grid, st);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_read(const Kv4ReadArgs& a, int sms, cudaStream_t st) {
-  const int grid = pair_grid(a.tokens, a.cache, sms);
-  if (a.cache.dim == 128) read_any<128>(a, grid, st);
-  else read_any<64>(a, grid, st);
+  const Kv4Cache& c = a.cache;
+  const dim3 grid = row_grid(a.tokens, c, sms);
+  if (c.dim == 64) {
+    if (c.group == 32) read_any<64, 32>(a, grid, st);
+    else read_any<64, 64>(a, grid, st);
+  } else {
+    if (c.group == 32) read_any<128, 32>(a, grid, st);
+    else if (c.group == 64) read_any<128, 64>(a, grid, st);
+    else read_any<128, 128>(a, grid, st);
+  }
   return cudaGetLastError();
 }
 
