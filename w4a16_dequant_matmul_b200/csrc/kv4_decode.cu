@@ -47,6 +47,18 @@
 namespace wq {
 namespace {
 
+// named_barrier, and whether any of its threads brought `flag`: one answer for all of them.
+__device__ __forceinline__ bool named_barrier_or(int id, int threads, bool flag) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(flag ? 1u : 0u)
+      : "memory");
+  return any != 0;
+}
+
 constexpr int kTile = 128;  // tokens per tile
 constexpr int kTileLog2 = 7;
 constexpr int kUnitCost = 2;  // places of a unit on the line before its first tile
