@@ -143,6 +143,37 @@ def test_append_and_read(dim, group, dtype, block, T, H):
             assert torch.equal(x.cpu(), torch.from_numpy(exact).float().to(out_dtype))
 
 
+@pytest.mark.parametrize("dim,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_append_where_codes_are_clipped(dim, group, dtype):
+    """A few groups whose end codes leave [0, 15] before the clipping (a range just above 15 S'
+    with ties at both ends, or a subnormal S' rounded far down) among ordinary ones, first in a
+    warp alone, then together."""
+    T, H, block = 96, 3, 64
+    x = rows(T, H, dim, dtype, 5).double()
+    x[3] = 1.0                                     # the other subnormal row of rows()
+    tie, low, far = (-7.5, 7.5), (-20 * 2.0 ** -24, 0.0), (-10 * 2.0 ** -24, 10 * 2.0 ** -24)
+    for t, h, g, ends in [(20, 1, 0, tie), (40, 2, dim // group - 1, low), (60, 0, 0, far),
+                          (61, 1, 0, tie), (61, 2, 0, low)]:
+        x[t, h, g * group:(g + 1) * group] = 0.0
+        x[t, h, g * group:g * group + 2] = torch.tensor(ends, dtype=torch.float64)
+    x = x.to(dtype)
+    q, s, z = quantized(x.double().numpy(), group)
+    exact = x.double().numpy().reshape(T, H, -1, group) / s[..., None]
+    level = np.rint(exact) + z[..., None]
+    assert (level > 15).any(-1).sum() >= 3 and (level < 0).any(-1).sum() >= 2  # the plan holds
+    v = x.flip(0).contiguous()
+    vq = quantized(v.double().numpy(), group)
+    blocks = -(-T // block)
+    cache = wq.wq_kv4_alloc(blocks, H, dim, group, block)
+    cache.fill_(0x5A)
+    want = cache.cpu().numpy().copy()
+    oracle.kv4_pack_cache(want, np.arange(T), (q, s, z), vq, block)
+    wq.wq_kv4_append(x.to(DEV), v.to(DEV), ints(np.arange(T)), cache, group=group)
+    ok()
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("dim,group,dtype", [(128, 128, BF16), (128, 32, F16), (64, 64, F16), (64, 32, BF16)])
 def test_append_many_equals_append_in_pieces(dim, group, dtype):
     """A call large enough for several rounds a warp stores what small calls do, tokens in any

@@ -4,6 +4,8 @@
 // ("DL S067 - Quantization", sections 1-2): one S', Z per group along the head dimension.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "../../include/wq.h"
 #include "common.cuh"
 #include "kv4.h"
@@ -161,7 +163,8 @@ __device__ __forceinline__ float2 widen(uint32_t w) {
 // RN(1/S') is within 2^-19 of it, and one FMA onto the 2^-13 grid (floats in [1024, 2048)) puts
 // a half-integer on itself and leaves the others on their side. Adding 1.5 2^23 - 1536 + Ze, Ze
 // the zero-point rounded up to even, rounds to an integer with ties to even k; the low byte is
-// code + (Z & 1).
+// code + (Z & 1). The clipping is left out where the caller knows that no code leaves [0, 15].
+template <bool kClip>
 __device__ __forceinline__ uint32_t encode8_snap(const float2 (&v)[4], float inv_s, int z) {
   const float z1 = static_cast<float>(z & 1);
   const float lo = 12582912.0f + z1, hi = lo + 15.0f;
@@ -172,12 +175,19 @@ __device__ __forceinline__ uint32_t encode8_snap(const float2 (&v)[4], float inv
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 x = __fadd2_rn(__ffma2_rn(v[j], inv2, g2), c2);
-    t[2 * j] = __float_as_uint(fminf(fmaxf(x.x, lo), hi));
-    t[2 * j + 1] = __float_as_uint(fminf(fmaxf(x.y, lo), hi));
+    t[2 * j] = __float_as_uint(kClip ? fminf(fmaxf(x.x, lo), hi) : x.x);
+    t[2 * j + 1] = __float_as_uint(kClip ? fminf(fmaxf(x.y, lo), hi) : x.y);
   }
   const uint32_t ev = __byte_perm(__byte_perm(t[0], t[2], 0x0040), __byte_perm(t[4], t[6], 0x0040), 0x5410);
   const uint32_t od = __byte_perm(__byte_perm(t[1], t[3], 0x0040), __byte_perm(t[5], t[7], 0x0040), 0x5410);
   return ev + (od << 4) - (z & 1u) * 0x11111111u;
+}
+
+// The code of a weight before it is clipped, by the same steps.
+__device__ __forceinline__ float code_level(float v, float inv_s, int z) {
+  const int odd = z & 1;
+  const float t = __fadd_rn(__fmaf_rn(v, inv_s, 1536.0f), 12581376.0f + static_cast<float>(z + odd));
+  return t - (12582912.0f + static_cast<float>(odd));
 }
 
 // How lanes share the rows of one kind (K or V) so that the stored order needs no exchange, or
@@ -281,8 +291,11 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 // The group's range is reduced in 16 bits, in the lane first, then over the lanes that share it.
 // S', Z and the codes are decided exactly, as in quantize.cu; the lanes that share groups decide
 // one each and hand the results round.
-// Bytes: 2 an element in, D/2 + 4 D/g a row out: 16384 tokens of 8 heads of 128 in 23 us, 3.7
-// TB/s (50 us with a word a lane); two rows a lane with the decisions shared between them: 25.
+// Codes are clipped only in warps with a group whose end codes leave [0, 15], as there (rare: a
+// tie at both ends, or a subnormal S').
+// Bytes: 2 an element in, D/2 + 4 D/g a row out: 16384 tokens of 8 heads of 128 in 20.9 us, 4.1
+// TB/s (50 us with a word a lane; 22.9 with every code clipped, 25 if two rows a lane share the
+// decisions too).
 template <int D, int G, bool kBf16, bool kV>
 __device__ __forceinline__ void append_rows(const Kv4AppendArgs& a) {
   using S = Share<D, G, kV>;
@@ -328,21 +341,32 @@ __device__ __forceinline__ void append_rows(const Kv4AppendArgs& a) {
       mx = own ? hi : mx;
     }
     const float2 l2 = widen<kBf16>(mn), h2 = widen<kBf16>(mx);
-    const AsymScale sz = asym_scale_zero(fmin_nan(0.0f, fmin_nan(l2.x, l2.y)),
-                                         fmax_nan(0.0f, fmax_nan(h2.x, h2.y)));
+    const float least = fmin_nan(0.0f, fmin_nan(l2.x, l2.y));
+    const float most = fmax_nan(0.0f, fmax_nan(h2.x, h2.y));
+    const AsymScale sz = asym_scale_zero(least, most);
     const uint32_t mine = sz.bad ? 0x80003C00u : sz.sbits | static_cast<uint32_t>(sz.z) << 16;
+    // codes grow with the weights: none is clipped unless those of the ends are
+    const int zero = static_cast<int>(sz.z);
+    const bool clip = __any_sync(0xffffffffu,
+                                 !sz.bad && (code_level(least, sz.inv_s, zero) < 0.0f ||
+                                             code_level(most, sz.inv_s, zero) > 15.0f));
     uint32_t word[S::kWords], got = mine;
     float inv_s = sz.inv_s;
+    auto encode = [&](auto clipped) {
 #pragma unroll
-    for (int u = 0; u < S::kWords; ++u) {
-      if (S::kGroups > 1 && u % kPer == 0) {
-        got = __shfl_sync(0xffffffffu, mine, share0 + u / kPer);
-        inv_s = __shfl_sync(0xffffffffu, sz.inv_s, share0 + u / kPer);
+      for (int u = 0; u < S::kWords; ++u) {
+        if (S::kGroups > 1 && u % kPer == 0) {
+          got = __shfl_sync(0xffffffffu, mine, share0 + u / kPer);
+          inv_s = __shfl_sync(0xffffffffu, sz.inv_s, share0 + u / kPer);
+        }
+        const float2 f[4] = {widen<kBf16>(x[u].x), widen<kBf16>(x[u].y), widen<kBf16>(x[u].z),
+                             widen<kBf16>(x[u].w)};
+        word[u] = got >> 31 ? 0u
+                            : encode8_snap<decltype(clipped)::value>(f, inv_s, (got >> 16) & 15);
       }
-      const float2 f[4] = {widen<kBf16>(x[u].x), widen<kBf16>(x[u].y), widen<kBf16>(x[u].z),
-                           widen<kBf16>(x[u].w)};
-      word[u] = got >> 31 ? 0u : encode8_snap(f, inv_s, (got >> 16) & 15);
-    }
+    };
+    if (clip) encode(std::true_type());
+    else encode(std::false_type());
     if constexpr (kV) {
       transpose4(word);
       if (D == 128) join_halves(word, l);
@@ -369,8 +393,8 @@ __device__ __forceinline__ void append_rows(const Kv4AppendArgs& a) {
 }
 
 // CTAs of 4 warps; at most 16 of a kind for each SM, then each goes on to further rows (65536
-// tokens of 8 heads of 128, append and fp32 read: 74 and 106 us; with 8: 78 and 128; with 4: 81
-// and 112).
+// tokens of 8 heads of 128, append with every code clipped and fp32 read: 74 and 106 us; with 8:
+// 78 and 128; with 4: 81 and 112).
 constexpr int kRowThreads = 128, kRowCtas = 16;
 
 // blockIdx.y: 0 the keys, 1 the values.
