@@ -681,3 +681,37 @@ def test_a_serving_run():
             at += new[b]
         ctx += np.array(new)
     assert kv.tolist() == ctx.tolist()
+
+
+# ------------------------------------------------------- ranges of scores and of value scales
+
+def refill(c, k, v):
+    """Other keys and values [kv, kv_heads, dim] (float) for a Case of one request."""
+    block = c.cache.shape[2] // (c.dim + 8 * c.dim // c.group)
+    at = torch.arange(c.kv_lens[0], device=DEV)
+    slots = (c.tables[0].long()[at // block] * block + at % block).int()
+    k, v = k.to(c.dtype), v.to(c.dtype)
+    wq.wq_kv4_append(k, v, slots, c.cache, group=c.group)
+    kk, vv = wq.wq_kv4_read(c.cache, slots, c.dim, group=c.group)
+    ok()
+    c.k, c.v = [kk.double().cpu().numpy()], [vv.double().cpu().numpy()]
+    x = k.double().unflatten(-1, (-1, c.group))
+    span = (x.amax(-1).clamp(min=0) - x.amin(-1).clamp(max=0)) / 15
+    c.smax = [float(torch.where(span < 2.0**-25, 1.0, span * (1 + 2.0**-11) + 2.0**-25).max())]
+
+
+@pytest.mark.parametrize("dim,group", SHAPES)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_score_and_value_scale_jump_in_one_tile(dim, group, dtype):
+    """The third tile of keys brings value scales 2^14 as large and scores far above all before:
+    the sums of the rows are rescaled for both in one step."""
+    kv, heads, kv_heads = 450, 8, 2
+    c = Case([kv], [33], heads, kv_heads, dim, group, 32, dtype, seed=12)
+    g = torch.Generator(device=DEV).manual_seed(12)
+    k, v = torch.randn(2, kv, kv_heads, dim, generator=g, device=DEV).unbind(0)
+    k[256:] *= 12
+    v[:256] *= 2.0**-7
+    v[256:] *= 2.0**7
+    refill(c, k, v)
+    c.check(*c.run())
+    ok()

@@ -462,6 +462,8 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
         for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
         tmem_st32(t_o + 32 * c, v);
       }
+      // it may run again in this step, and a load is not ordered behind a store in flight
+      tmem_wait_st();
     };
     for (int j = 0; j < u.nt; ++j) {
       if (!wait_warp(&ctl->s_full[i], j & 1, ctl, a.status) ||
