@@ -715,3 +715,35 @@ def test_score_and_value_scale_jump_in_one_tile(dim, group, dtype):
     refill(c, k, v)
     c.check(*c.run())
     ok()
+
+
+def test_calls_on_given_streams():
+    """Calls with `stream=` from one current stream, on two others in turn, each with a workspace
+    and results of its own: a long request split over the grid, so that every call has parts in
+    its workspace, as results under the stream and after other allocations of the current one."""
+    c = Case([6000, 77], [1, 2], 8, 2, 128, 128, 32, BF16, seed=13)
+    want, wlse = c.run()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    slots = ints(np.arange(64))
+    k, v = wq.wq_kv4_read(c.cache, slots, 128)
+    x = torch.randn(64, 2, 128, device=DEV).to(BF16)
+    other = [torch.zeros_like(c.cache) for _ in streams]
+    free, ctx, new = ints(np.arange(10)), ints([0, 0]), ints([100, 40])
+    tab = [torch.full((2, 8), -1, dtype=torch.int32, device=DEV) for _ in streams]
+    wq.wq_kv4_append(x, x, slots, want_cache := torch.zeros_like(c.cache))
+    wtab = tab[0].clone()
+    wslots = wq.wq_kv4_block_tables(ctx, new, free, wtab, 16, 150)[0]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(20):
+        for s, t, o in zip(streams, tab, other):
+            outs.append((*c.run(stream=s), *wq.wq_kv4_read(c.cache, slots, 128, stream=s),
+                         wq.wq_kv4_block_tables(ctx, new, free, t, 16, 150, stream=s)[0]))
+            wq.wq_kv4_append(x, x, slots, o, stream=s)
+            torch.full((1 << 20,), -1.0, device=DEV)  # takes up what the current stream let go
+    torch.cuda.synchronize()
+    ok()
+    for got in outs:
+        for a, b in zip(got, (want, wlse, k, v, wslots)):
+            assert torch.equal(a, b)
+    assert all(torch.equal(t, wtab) for t in tab) and all(torch.equal(o, want_cache) for o in other)

@@ -237,3 +237,67 @@ def test_oracle_block_tables_pin():
     assert t.tolist() == [[7, 2, -1], [-1, -1, -1], [9, 4, -1]]
     assert slots.tolist() == [7 * 16 + 15, 32, 33] + [9 * 16 + i for i in range(16)] + [64, -1, -1]
     assert starts.tolist() == [0, 3, 3, 20] and kv.tolist() == [18, 0, 17] and taken == 3
+
+
+def test_binding_allocates_on_the_given_stream(monkeypatch):
+    """With `stream`, that stream is the current one while a call allocates its results and its
+    workspace (torch hands memory of one stream to that stream's later work only), and the call
+    runs on it; without, or where it is current already, nothing changes. Host-side stand-ins."""
+    current, seen = [70], []
+
+    class Stream:
+        def __init__(self, handle, index):
+            self.cuda_stream, self.device = handle, torch.device("cuda", index)
+
+    class Current:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            self.prev, current[0] = current[0], self.s.cuda_stream
+
+        def __exit__(self, *exc):
+            current[0] = self.prev
+
+    def empty(shape, strides, dtype, device):
+        seen.append(("alloc", current[0]))
+        return torch.empty(shape, dtype=dtype)
+
+    k = wq._kv4()
+    stub = type("Stub", (), dict(vars(k)))()
+    stub.current_device, stub.raw_stream = lambda: 0, lambda d: current[0]
+    stub.empty, stub.workspace_bytes = empty, {0: 16}
+    for name in ("block_tables", "append", "read", "attention"):
+        setattr(stub, name, lambda *args, name=name: seen.append((name, args[-1])) or 0)
+    stub.on_stream = Current
+    monkeypatch.setattr(wq, "_KV4", stub)
+
+    class OnZero(torch.Tensor):
+        """A host tensor that says it is on device 0."""
+        def get_device(self):
+            return 0
+
+        device = property(lambda self: 0)
+
+    zero = lambda t: t.as_subclass(OnZero)  # noqa: E731
+    ints = lambda *s: zero(torch.zeros(s, dtype=torch.int32))  # noqa: E731
+    c = zero(wq.wq_kv4_alloc(4, 2, 64, 32, 16, device="cpu"))
+    x = zero(torch.zeros(3, 2, 64, dtype=torch.bfloat16))
+
+    def calls(stream):
+        seen.clear()
+        wq.wq_kv4_append(x, x, ints(3), c, group=32, stream=stream)
+        wq.wq_kv4_read(c, ints(3), 64, group=32, stream=stream)
+        wq.wq_kv4_block_tables(ints(2), ints(2), ints(4), ints(2, 4), 16, 8, stream=stream)
+        wq.wq_kv4_attention(x, c, ints(1, 4), ints(2), ints(1), 3, group=32, return_lse=True,
+                            stream=stream)
+        assert current == [70]
+        return list(seen)
+
+    for stream, handle in ((None, 70), (Stream(70, 0), 70), (Stream(88, 0), 88)):
+        alloc = ("alloc", handle)
+        assert calls(stream) == [("append", handle), alloc, alloc, ("read", handle), alloc,
+                                 ("block_tables", handle), alloc, alloc, alloc,
+                                 ("attention", handle)]
+    with pytest.raises(ValueError):  # a stream of another device
+        calls(Stream(88, 1))

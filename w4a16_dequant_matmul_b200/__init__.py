@@ -26,6 +26,8 @@ Functions carry the C names:
     wq_kv4_attention(Q, cache, tables, q_starts, kv_lens, max_q, group, ...) -> out
     wq_get_status() -> int
 S and Z are returned as torch.float16 tensors (binary16 bit patterns in the C ABI).
+A wq_kv4_ call given a `stream` is as one made under torch.cuda.stream(stream): it runs there,
+and its results and its workspace belong to that stream.
 """
 from __future__ import annotations
 
@@ -491,7 +493,7 @@ class _Kv4Names:
         self.empty = torch.empty_strided
         self.code = {torch.bfloat16: WQ_BF16, torch.float16: WQ_F16}
         self.out_code = {torch.float32: WQ_F32, torch.bfloat16: WQ_BF16, torch.float16: WQ_F16}
-        self.device = torch.cuda.device
+        self.device, self.on_stream = torch.cuda.device, torch.cuda.stream
         self.current_device = getattr(torch._C, "_cuda_getDevice", None) or \
             torch.cuda.current_device
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -512,14 +514,21 @@ def _kv4():
 
 
 def _kv4_stream(k, t, stream):
-    """Handle of `stream`, or of the current stream of t's device; None where that device is not
-    the current one (the caller then makes it so and calls itself again)."""
+    """Handle of the current stream where `stream` (None: any) and t's device are the current
+    ones; else a context that makes them so, in which the caller calls itself again without a
+    stream. What a call allocates (results, workspace) so belongs to the stream that it runs on:
+    torch hands memory that is let go only to later work of the stream that it belongs to."""
     d = t.get_device()
     if d < 0:  # a host tensor: the library rejects it; any stream will do
         return 0
-    if d != k.current_device():
-        return None
-    return k.raw_stream(d) if stream is None else stream.cuda_stream
+    if stream is not None:
+        if stream.device.index != d:
+            raise ValueError(f"the stream is of {stream.device}, the tensors of device {d}")
+        if d != k.current_device() or stream.cuda_stream != k.raw_stream(d):
+            return k.on_stream(stream)
+    elif d != k.current_device():
+        return k.device(t.device)
+    return k.raw_stream(d)
 
 
 def _kv4_bad_ints(t, name, n):
@@ -597,10 +606,10 @@ def wq_kv4_block_tables(ctx_lens, new_lens, free_blocks, tables, block_size: int
     token are -1."""
     k = _KV4 or _kv4()
     handle = _kv4_stream(k, ctx_lens, stream)
-    if handle is None:
-        with k.device(ctx_lens.device):
+    if handle.__class__ is not int:
+        with handle:
             return wq_kv4_block_tables(ctx_lens, new_lens, free_blocks, tables, block_size,
-                                       n_slots, stream)
+                                       n_slots)
     i32 = k.int32
     B = ctx_lens.shape[0]
     if ctx_lens.dtype is not i32 or ctx_lens.dim() != 1 or not ctx_lens.is_contiguous():
@@ -627,9 +636,9 @@ def wq_kv4_append(K, V, slots, cache, group: int = None, stream=None) -> None:
     strides) into slots (int32 [T], negative: skipped) of the cache."""
     k = _KV4 or _kv4()
     handle = _kv4_stream(k, K, stream)
-    if handle is None:
-        with k.device(K.device):
-            return wq_kv4_append(K, V, slots, cache, group, stream)
+    if handle.__class__ is not int:
+        with handle:
+            return wq_kv4_append(K, V, slots, cache, group)
     T, h, d, kt, kh = _kv4_heads(K, "K")
     if V.shape != K.shape or V.dtype is not K.dtype:
         raise ValueError("K and V must have one shape and dtype")
@@ -650,9 +659,9 @@ def wq_kv4_read(cache, slots, head_dim: int, group: int = None, out_dtype=None, 
     [T, kv_heads, head_dim] float32 (exact), bfloat16 or float16."""
     k = _KV4 or _kv4()
     handle = _kv4_stream(k, cache, stream)
-    if handle is None:
-        with k.device(cache.device):
-            return wq_kv4_read(cache, slots, head_dim, group, out_dtype, stream)
+    if handle.__class__ is not int:
+        with handle:
+            return wq_kv4_read(cache, slots, head_dim, group, out_dtype)
     out_dtype = k.float32 if out_dtype is None else out_dtype
     if slots.dtype is not k.int32 or slots.dim() != 1 or not slots.is_contiguous():
         _kv4_bad_ints(slots, "slots", ("T",))
@@ -683,10 +692,10 @@ def wq_kv4_attention(Q, cache, tables, q_starts, kv_lens, max_q: int, group: int
     left as they were."""
     k = _KV4 or _kv4()
     handle = _kv4_stream(k, Q, stream)
-    if handle is None:
-        with k.device(Q.device):
+    if handle.__class__ is not int:
+        with handle:
             return wq_kv4_attention(Q, cache, tables, q_starts, kv_lens, max_q, group, scale,
-                                    causal, window, out, return_lse, workspace, stream)
+                                    causal, window, out, return_lse, workspace)
     T, heads, d, qt, qh = _kv4_heads(Q, "Q")
     c = _kv4_cache(cache, d, group)
     B = kv_lens.shape[0]
