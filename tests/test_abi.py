@@ -244,3 +244,64 @@ def test_binding_makes_the_tensors_device_current(monkeypatch):
     X0, P0, S0, Y0 = (_FakeCudaTensor(t.shape, 0) for t in (X, P, S, Y))
     wq.wq_w4a16_gemm(X0, P0, S0, S0, 128, Y=Y0, stream=_Stream())
     assert seen == [1, 0]
+
+
+def test_binding_allocates_on_the_given_stream(monkeypatch):
+    """With `stream`, that stream is current while a call allocates its results and workspace:
+    torch hands memory of one stream only to that stream's later work (host-side stand-ins)."""
+    import torch
+
+    current, seen = [None], []
+
+    class _Stream:
+        cuda_stream = 88
+
+    class _Current:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            current[0] = self.s
+
+        def __exit__(self, *exc):
+            current[0] = None
+
+    class _Lib:
+        def __getattr__(self, name):
+            if name.endswith("_bytes"):
+                return lambda *args: 64
+            return lambda *args: seen.append(name) or 0
+
+    real = torch.empty
+
+    def empty(*args, **kw):
+        seen.append(current[0])
+        return real(*args, **kw)
+
+    W, X = torch.zeros(4, 128), torch.zeros(3, 128, dtype=torch.bfloat16)
+    P, S, s = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 1).half(), torch.ones(128)
+    stream = _Stream()
+    monkeypatch.setattr(wq, "lib", lambda: _Lib())
+    monkeypatch.setattr(wq, "_GEMM", _Lib().wq_w4a16_gemm)
+    monkeypatch.setattr(torch.cuda, "stream", _Current)
+    monkeypatch.setattr(torch, "empty", empty)
+    for f, name, n in (
+            (lambda: wq.wq_quantize_rtn_g128(W, stream=stream), "wq_quantize_rtn_g128", 3),
+            (lambda: wq.wq_quantize_rtn_g128(W, 8, 128, False, stream=stream), "wq_quantize_rtn_g128", 2),
+            (lambda: wq.wq_quantize_rtn_per_tensor(W, stream=stream), "wq_quantize_rtn_per_tensor", 4),
+            (lambda: wq.wq_quantize_rtn_per_tensor_noalloc(W, stream=stream),
+             "wq_quantize_rtn_per_tensor_noalloc", 3),
+            (lambda: wq.wq_pack_int4(P, stream=stream), "wq_pack_int4", 1),
+            (lambda: wq.wq_dequant(P, S, S, stream=stream), "wq_dequant", 1),
+            (lambda: wq.wq_w4a16_gemm(X, P, S, S, stream=stream), "wq_w4a16_gemm", 1),
+            (lambda: wq.wq_w8a16_gemm(X, W.char(), S, stream=stream), "wq_w8a16_gemm", 1),
+            (lambda: wq.wq_channel_stat(W, stream=stream), "wq_channel_stat", 1),
+            (lambda: wq.wq_smooth_scales(s, s, stream=stream), "wq_smooth_scales", 1),
+            (lambda: wq.wq_awq_scales(s, 0.5, stream=stream), "wq_awq_scales", 1),
+            (lambda: wq.wq_quantize_rtn_scaled(W, s, stream=stream), "wq_quantize_rtn_scaled", 3),
+            (lambda: wq.wq_scale_activations(X, s, stream=stream), "wq_scale_activations", 1),
+            (lambda: wq.wq_quantize_gptq(W, X, stream=stream), "wq_quantize_gptq", 4)):
+        seen.clear()
+        f()
+        assert seen == [stream] * n + [name], name
+        assert current == [None]

@@ -26,8 +26,8 @@ Functions carry the C names:
     wq_kv4_attention(Q, cache, tables, q_starts, kv_lens, max_q, group, ...) -> out
     wq_get_status() -> int
 S and Z are returned as torch.float16 tensors (binary16 bit patterns in the C ABI).
-A wq_kv4_ call given a `stream` is as one made under torch.cuda.stream(stream): it runs there,
-and its results and its workspace belong to that stream.
+A call given a `stream` runs there, and what it allocates (results, workspace) belongs to that
+stream, as under torch.cuda.stream(stream).
 """
 from __future__ import annotations
 
@@ -200,6 +200,17 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for work on `stream` (None: the current one). It belongs to that stream, so that
+    torch hands it, once let go, to later work of that stream only."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _rows(t, name):
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
@@ -236,13 +247,13 @@ def wq_quantize_rtn_g128(W, w_bit: int = 4, group: int = 128, zero_point: bool =
     ldw = _rows(W, "W")
     dev = W.device
     if w_bit == 4:
-        packed = torch.empty((N, K // 2), dtype=torch.uint8, device=dev) if packed is None else packed
+        packed = _empty((N, K // 2), torch.uint8, dev, stream) if packed is None else packed
         G = K // group if group else 1
-        S = torch.empty((N, G), dtype=torch.float16, device=dev) if S is None else S
-        Z = torch.empty((N, G), dtype=torch.float16, device=dev) if Z is None else Z
+        S = _empty((N, G), torch.float16, dev, stream) if S is None else S
+        Z = _empty((N, G), torch.float16, dev, stream) if Z is None else Z
     else:
-        packed = torch.empty((N, K), dtype=torch.int8, device=dev) if packed is None else packed
-        S = torch.empty((N,), dtype=torch.float16, device=dev) if S is None else S
+        packed = _empty((N, K), torch.int8, dev, stream) if packed is None else packed
+        S = _empty((N,), torch.float16, dev, stream) if S is None else S
     p = _QParams(w_bit, group, 1 if zero_point else 0)
     with _on_device(W):
         st = lib().wq_quantize_rtn_g128(_ptr(W), _w_dtype(W), N, K, ldw, ctypes.byref(p),
@@ -262,12 +273,12 @@ def wq_quantize_rtn_per_tensor(W, workspace=None, stream=None):
     N, K = W.shape
     ldw = _rows(W, "W")
     dev = W.device
-    packed = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
-    S = torch.empty((1,), dtype=torch.float16, device=dev)
-    Z = torch.empty((1,), dtype=torch.float16, device=dev)
+    packed = _empty((N, K // 2), torch.uint8, dev, stream)
+    S = _empty((1,), torch.float16, dev, stream)
+    Z = _empty((1,), torch.float16, dev, stream)
     nbytes = wq_quantize_per_tensor_workspace_bytes(N, K)
     if workspace is None:
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        workspace = _empty((nbytes,), torch.uint8, dev, stream)
     with _on_device(W):
         st = lib().wq_quantize_rtn_per_tensor(_ptr(W), _w_dtype(W), N, K, ldw, _ptr(packed),
                                               _ptr(S), _ptr(Z), _ptr(workspace),
@@ -286,9 +297,9 @@ def wq_quantize_rtn_per_tensor_noalloc(W, stream=None):
 
     N, K = W.shape
     ldw = _rows(W, "W")
-    packed = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
-    S = torch.empty((1,), dtype=torch.float16, device=W.device)
-    Z = torch.empty((1,), dtype=torch.float16, device=W.device)
+    packed = _empty((N, K // 2), torch.uint8, W.device, stream)
+    S = _empty((1,), torch.float16, W.device, stream)
+    Z = _empty((1,), torch.float16, W.device, stream)
     with _on_device(W):
         st = lib().wq_quantize_rtn_per_tensor_noalloc(_ptr(W), _w_dtype(W), N, K, ldw,
                                                       _ptr(packed), _ptr(S), _ptr(Z),
@@ -304,7 +315,7 @@ def wq_pack_int4(codes, packed=None, stream=None):
     N, K = codes.shape
     if not codes.is_contiguous():
         raise ValueError("codes must be contiguous")
-    packed = torch.empty((N, K // 2), dtype=torch.uint8, device=codes.device) if packed is None else packed
+    packed = _empty((N, K // 2), torch.uint8, codes.device, stream) if packed is None else packed
     with _on_device(codes):
         st = lib().wq_pack_int4(_ptr(codes), N, K, _ptr(packed), _stream(stream))
     _check(st, "wq_pack_int4")
@@ -319,7 +330,7 @@ def wq_dequant(packed, S, Z, group: int = 128, out_dtype=None, out=None, stream=
     N, K2 = packed.shape
     K = 2 * K2
     code = WQ_F32 if out_dtype == torch.float32 else WQ_BF16 if out_dtype == torch.bfloat16 else -1
-    out = torch.empty((N, K), dtype=out_dtype, device=packed.device) if out is None else out
+    out = _empty((N, K), out_dtype, packed.device, stream) if out is None else out
     with _on_device(packed):
         st = lib().wq_dequant(_ptr(packed), _ptr(S), _ptr(Z), N, K, group, _ptr(out), code,
                               _stream(stream))
@@ -342,7 +353,7 @@ def wq_w4a16_gemm(X, packed, S, Z, group: int = 128, Y=None, stream=None):
     if Y is None:
         import torch
 
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+        Y = _empty((M, N), torch.bfloat16, X.device, stream)
     ldy = _rows(Y, "Y")
     with _on_device(X):
         st = _GEMM(X.data_ptr(), M, ldx, packed.data_ptr(), S.data_ptr(), Z.data_ptr(), N, K,
@@ -359,7 +370,7 @@ def wq_w8a16_gemm(X, codes, S, Y=None, stream=None):
     M, K = X.shape
     N = codes.shape[0]
     ldx = _rows(X, "X")
-    Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device) if Y is None else Y
+    Y = _empty((M, N), torch.bfloat16, X.device, stream) if Y is None else Y
     ldy = _rows(Y, "Y")
     with _on_device(X):
         st = lib().wq_w8a16_gemm(_ptr(X), M, ldx, _ptr(codes), _ptr(S), N, K, _ptr(Y), ldy,
@@ -375,7 +386,7 @@ def wq_channel_stat(A, stat: int = WQ_STAT_ABSMAX, out=None, stream=None):
 
     rows, cols = A.shape
     lda = _rows(A, "A")
-    out = torch.empty((cols,), dtype=torch.float32, device=A.device) if out is None else out
+    out = _empty((cols,), torch.float32, A.device, stream) if out is None else out
     with _on_device(A):
         st = lib().wq_channel_stat(_ptr(A), _w_dtype(A), rows, cols, lda, int(stat), _ptr(out),
                                    _stream(stream))
@@ -388,7 +399,7 @@ def wq_smooth_scales(xmax, wmax, alpha: float = 0.5, out=None, stream=None):
     import torch
 
     K = xmax.shape[0]
-    out = torch.empty((K,), dtype=torch.float32, device=xmax.device) if out is None else out
+    out = _empty((K,), torch.float32, xmax.device, stream) if out is None else out
     with _on_device(xmax):
         st = lib().wq_smooth_scales(_ptr(xmax), _ptr(wmax), K, float(alpha), _ptr(out),
                                     _stream(stream))
@@ -401,7 +412,7 @@ def wq_awq_scales(a_mag, alpha: float, out=None, stream=None):
     import torch
 
     K = a_mag.shape[0]
-    out = torch.empty((K,), dtype=torch.float32, device=a_mag.device) if out is None else out
+    out = _empty((K,), torch.float32, a_mag.device, stream) if out is None else out
     with _on_device(a_mag):
         st = lib().wq_awq_scales(_ptr(a_mag), K, float(alpha), _ptr(out), _stream(stream))
     _check(st, "wq_awq_scales")
@@ -418,9 +429,9 @@ def wq_quantize_rtn_scaled(W, s, group: int = 128, zero_point: bool = True, pack
     ldw = _rows(W, "W")
     dev = W.device
     G = K // group if group else 1
-    packed = torch.empty((N, K // 2), dtype=torch.uint8, device=dev) if packed is None else packed
-    S = torch.empty((N, G), dtype=torch.float16, device=dev) if S is None else S
-    Z = torch.empty((N, G), dtype=torch.float16, device=dev) if Z is None else Z
+    packed = _empty((N, K // 2), torch.uint8, dev, stream) if packed is None else packed
+    S = _empty((N, G), torch.float16, dev, stream) if S is None else S
+    Z = _empty((N, G), torch.float16, dev, stream) if Z is None else Z
     p = _QParams(4, group, 1 if zero_point else 0)
     with _on_device(W):
         st = lib().wq_quantize_rtn_scaled(_ptr(W), _w_dtype(W), N, K, ldw, _ptr(s),
@@ -437,7 +448,7 @@ def wq_scale_activations(X, s, out=None, stream=None):
 
     M, K = X.shape
     ldx = _rows(X, "X")
-    out = torch.empty((M, K), dtype=torch.bfloat16, device=X.device) if out is None else out
+    out = _empty((M, K), torch.bfloat16, X.device, stream) if out is None else out
     ldo = _rows(out, "out")
     with _on_device(X):
         st = lib().wq_scale_activations(_ptr(X), M, K, ldx, _ptr(s), _ptr(out), ldo,
@@ -461,12 +472,12 @@ def wq_quantize_gptq(W, X, group: int = 128, zero_point: bool = True, damp: floa
     ldw = _rows(W, "W")
     ldx = _rows(X, "X")
     dev = W.device
-    packed = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
-    S = torch.empty((N, K // group), dtype=torch.float16, device=dev)
-    Z = torch.empty((N, K // group), dtype=torch.float16, device=dev)
+    packed = _empty((N, K // 2), torch.uint8, dev, stream)
+    S = _empty((N, K // group), torch.float16, dev, stream)
+    Z = _empty((N, K // group), torch.float16, dev, stream)
     nbytes = wq_gptq_workspace_bytes(N, K)
     if workspace is None:
-        workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dev)
+        workspace = _empty((max(nbytes, 16),), torch.uint8, dev, stream)
     p = _QParams(4, group, 1 if zero_point else 0)
     with _on_device(W):
         st = lib().wq_quantize_gptq(_ptr(W), _w_dtype(W), N, K, ldw, _ptr(X), T, ldx,
