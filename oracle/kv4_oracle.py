@@ -66,9 +66,11 @@ def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None):
     x (16 + q_code) S scale with 16 + q_code <= 31, minus x-sum (16 + Z) S scale, or of the
     products with both 16-bit parts of S (q - Z): each step and each of about 8 further fp32
     operations errs by at most 2^-23 of the largest magnitude in it, at most 31 S scale sum|x|
-    (`s_max`: the largest S of the request's keys); a binary16 part of S (q - Z) / 16 may be a
-    subnormal, half a step of 2^-24 off. That makes every probability wrong by a relative
-        e = ((D/8 + 8) 2^-23 31 S + 2^-21) scale sum|x|
+    (`s_max`: the largest S of the request's keys). Binary16 parts are of S (q - Z) 2^-E with the
+    largest S 2^-E of the row's groups at 2^11 at least; S 2^-E of another may be a subnormal,
+    half a step of 2^-24 off, times 15: 2^-32 of the largest S. That makes every probability
+    wrong by a relative
+        e = ((D/8 + 8) 2^-23 31 + 2^-32) S scale sum|x|
     at most, and numerator and denominator by e each; with it 2^-11 for its rounding to binary16
     (half a step) and 2^-11 for that of its value, 2^-20 for exp2, log2 and the scale products, and (kv/16 + 64) 2^-23 for the two fp32 sums over the keys. The error of out is
     that times sum_j p_j |v_j|. Where a rounded p is a binary16 subnormal it errs by half its
@@ -99,7 +101,7 @@ def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None):
             lse[i, h] = m + np.log(l)
             e = 0.0
             if s_max is not None:
-                e = ((dim / 8 + 8) * 2.0**-23 * 31 * s_max + 2.0**-21) * abs(scale) * np.abs(q[i, h]).sum()
+                e = ((dim / 8 + 8) * 2.0**-23 * 31 + 2.0**-32) * s_max * abs(scale) * np.abs(q[i, h]).sum()
             rel = 2 * e + 2.0**-10 + 2.0**-20 + (kv / 16 + 64) * 2.0**-23
             low = ((last + 1 - first) * 2.0**-31 / l + 2.0**-29) * 2.2 * np.abs(vv).max()
             bound[i, h] = rel * (p @ np.abs(vv) / l) + low

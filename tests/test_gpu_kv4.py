@@ -747,3 +747,24 @@ def test_calls_on_given_streams():
         for a, b in zip(got, (want, wlse, k, v, wslots)):
             assert torch.equal(a, b)
     assert all(torch.equal(t, wtab) for t in tab) and all(torch.equal(o, want_cache) for o in other)
+
+
+@pytest.mark.parametrize("dim,group", SHAPES)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("spread", [3e-3, 2e-4, 1e-5, 6e3])
+def test_small_and_large_keys(dim, group, dtype, spread):
+    """Keys from where their scales are binary16 subnormals to where S (q - Z) nears the largest
+    binary16 number, with a softmax scale that brings the scores back to a few units: as a
+    prompt and, by a max_q of 0, on the kernel for few rows. Groups of a key lie up to 2^6
+    apart."""
+    kv, heads, kv_heads = 200, 4, 2
+    c = Case([kv], [20], heads, kv_heads, dim, group, 16, dtype, seed=14)
+    g = torch.Generator(device=DEV).manual_seed(14)
+    k, v = torch.randn(2, kv, kv_heads, dim, generator=g, device=DEV).unbind(0)
+    apart = torch.randint(0, 7, (kv, kv_heads, dim // group, 1), generator=g, device=DEV)
+    k = (k.unflatten(-1, (-1, group)) * torch.exp2(-apart.float())).flatten(-2) * spread
+    refill(c, k, v)
+    scale = dim**-0.5 / spread
+    for max_q in (20, 0):
+        c.check(*c.run(scale=scale, max_q=max_q), scale=scale)
+    ok()

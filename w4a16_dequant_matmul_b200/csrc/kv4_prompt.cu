@@ -9,7 +9,10 @@
 // Where a key's row has one scale, K is its codes less Z, exact in 16 bits, and the scale meets
 // the score in fp32 (ks = S_k scale log2(e)). With several, K is S_k (q - Z) as a sum of two
 // 16-bit numbers (15 bits in all, so the sum is exact) and the product runs twice; ks is then
-// one number. For bf16 results V is S_v (q - Z) 2^-E rounded once to binary16 (half a step is 2^-11,
+// one number for bf16. binary16 has no room for every S_k (q - Z): there each key has a power of
+// two of its own that brings its largest S_k into [2^11, 2^12), and ks is the key's again. (A
+// fixed 2^-4 had made S_k below 2^-10 binary16 subnormals: 0.3 % off at 2e-5, 0 at 2^-21.)
+// For bf16 results V is S_v (q - Z) 2^-E rounded once to binary16 (half a step is 2^-11,
 // an eighth of out's); for fp16 results that would show, so V stays exact: with one scale the
 // codes less Z, S_v 2^-E meeting p, with several a sum of two numbers as for K. E is the
 // exponent of the largest S_v so far: one number for all rows, which moves rarely (O is
@@ -91,13 +94,14 @@ struct Ctl {
 template <int D, int G, bool kBf16>
 struct Cfg {
   static constexpr bool kSplitK = G > 1;            // K = hi + lo
+  static constexpr bool kKeyScale = !kSplitK || !kBf16;  // ks is the key's own
   static constexpr bool kSplitV = G > 1 && !kBf16;  // V = hi + lo
   static constexpr bool kScaleP = G == 1 && !kBf16; // S_v 2^-E meets p
   static constexpr int kKBufs = kSplitK ? 1 : 2;
   static constexpr int kVBufs = kSplitV ? 1 : 2;
   static constexpr int kQBytes = kM * D * 2;  // one Q tile
   static constexpr int kTBytes = kN * D * 2;  // one K tile, one V^T tile; hi and lo are two
-  static constexpr int kVecFloats = (kSplitK ? 0 : kN) + (kScaleP ? kN : 0);  // ks, S_v 2^-E
+  static constexpr int kVecFloats = (kKeyScale ? kN : 0) + (kScaleP ? kN : 0);  // ks, S_v 2^-E
   static constexpr int kRawK = kN * (D / 2 + 8 * G);  // K codes, K and V scale words of a tile
   static constexpr int kRawV = kN * (D / 2 + 4 * G);  // V codes, V scale words
   static constexpr int kSmem = 1024 + 2 * kQBytes + 4 * kTBytes + kRawK + kRawV +
@@ -175,6 +179,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 __device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+
+// The exponent of a positive binary16 number (of its smallest for 0), and a power of two.
+__device__ __forceinline__ int half_exponent(uint32_t bits) {
+  return static_cast<int>(__float_as_uint(f16_bits_to_f32(max(bits, 1u))) >> 23) - 127;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((127 + e) << 23); }
 
 // Eight codes of a word less Z as 16-bit floats, pairs (i, i + 4). zz: Z + 128 (bf16) or
 // Z + 1024 (fp16) twice; zh: -(Z + 64) twice (fp16).
@@ -447,8 +457,6 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
     const uint32_t t_s = t_row + i * kN;
     const uint32_t t_o = t_row + 2 * kN + i * 128;
     const uint32_t vec_s = smem_u32(vec);
-    // K of fp16 with several scales is taken times 2^-4, so that no S_k (q - Z) overflows
-    const float k1 = a.scale_log2 * (kBf16 ? 1.0f : 16.0f);
     float m = -INFINITY, l = 0.0f;
     int exponent = 0;
     bool ok = true;
@@ -488,11 +496,12 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
       for (int pass = 0; pass < 3; ++pass) {
         const float ref = m == -INFINITY ? 0.0f : m;
         const float mx =
-            safe ? row_pass<!C::kSplitK, C::kScaleP, false>(t_s, vs, k1, kLift - ref, 0, 0, 0,
-                                                            there, p, sum)
-                 : row_pass<!C::kSplitK, C::kScaleP, true>(t_s, vs, k1, kLift - ref, pos0, lim,
-                                                           a.window > 0 ? lim - a.window : -1,
-                                                           there, p, sum);
+            safe ? row_pass<C::kKeyScale, C::kScaleP, false>(t_s, vs, a.scale_log2, kLift - ref,
+                                                             0, 0, 0, there, p, sum)
+                 : row_pass<C::kKeyScale, C::kScaleP, true>(t_s, vs, a.scale_log2, kLift - ref,
+                                                            pos0, lim,
+                                                            a.window > 0 ? lim - a.window : -1,
+                                                            there, p, sum);
         // mx is relative to m: above kLift + kHeadroom m has to move (from -inf: always)
         const bool over = m == -INFINITY ? mx > -INFINITY : mx > kLift + kHeadroom;
         if (!__any_sync(0xffffffffu, over)) break;
@@ -595,21 +604,27 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
         }
         y = __reduce_max_sync(0xffffffffu, y);  // alike in the four warps
         if (y != 0) {
-          const int top = static_cast<int>(__float_as_uint(f16_bits_to_f32(y)) >> 23) - 127;
+          const int top = half_exponent(y);
           if (top - exponent > kMost) exponent = top - kTop;
         }
         if (e == 0) ctl->exponent[j & 3] = exponent < -60 ? 0 : exponent;
       }
       const float down = exponent < -60 ? 0.0f : ex2(static_cast<float>(-exponent));
       {
-        uint32_t zz[G], zh[G], sh[G], sl[G];
-        float s0 = 0.0f;
+        uint32_t words[G], zz[G], zh[G], sh[G], sl[G];
+        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          const uint32_t sz = k_there ? lds32(rk_sz + 4 * (G * e + i)) : 0u;
-          const uint32_t z = sz >> 16, z2 = z | z << 16;
-          const float s = f16_bits_to_f32(sz & 0xFFFFu);
-          if (i == 0) s0 = s;
+          words[i] = k_there ? lds32(rk_sz + 4 * (G * e + i)) : 0u;
+          top = max(top, words[i] & 0xFFFFu);
+        }
+        // binary16 parts: the key's exponent, S_k 2^-ek (q - Z) < 2^16
+        const int ek = C::kSplitK && !kBf16 ? half_exponent(top) - 11 : 0;
+        const float ks = C::kSplitK ? pow2(ek) : f16_bits_to_f32(top);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          const uint32_t z = words[i] >> 16, z2 = z | z << 16;
+          const float s = f16_bits_to_f32(words[i] & 0xFFFFu);
           // Z as a binary16 integer: to Z + 128 in bf16, Z + 1024 and -(Z + 64) in binary16
           if (kBf16) {
             const float zf = f16_bits_to_f32(z) + 128.0f;
@@ -620,7 +635,7 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
           } else {
             zz[i] = hfma2(z2, 0x3C003C00u, 0x64006400u);
             zh[i] = hfma2(z2, 0xBC00BC00u, 0xD400D400u);
-            sh[i] = half2_bits(s * 0.0625f, s * 0.0625f);
+            sh[i] = half2_bits(s * pow2(-ek), s * pow2(-ek));
           }
         }
         const uint32_t dst = sK0 + kb * C::kTBytes + e * 128;
@@ -665,7 +680,7 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
           }
         }
         const uint32_t vs = vec0 + (j & 3) * C::kVecFloats * 4 + e * 4;
-        if (!C::kSplitK) sts_f32(vs, s0 * a.scale_log2);
+        if (C::kKeyScale) sts_f32(vs, ks * a.scale_log2);
         if (C::kScaleP) {
           const uint32_t sv = k_there ? lds32(rk_szv + 4 * e) : 0u;
           sts_f32(vs + kN * 4, f16_bits_to_f32(sv & 0xFFFFu) * down);
