@@ -768,3 +768,54 @@ def test_small_and_large_keys(dim, group, dtype, spread):
     for max_q in (20, 0):
         c.check(*c.run(scale=scale, max_q=max_q), scale=scale)
     ok()
+
+
+@pytest.mark.parametrize("dim,group", SHAPES)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("where", ["later", "one_later", "behind", "zeros", "mixed"])
+def test_value_scales_that_a_row_does_not_see(dim, group, dtype, where):
+    """Values 2^22 as large on keys that most rows of the tile do not see (later ones, one only,
+    those behind the window) take no bits from the others; rows of zeros (S' = 1) and scales from
+    all over the range among small values."""
+    kv, heads, kv_heads, window = 230, 4, 2, 0
+    c = Case([kv], [kv if where in ("later", "one_later") else 100], heads, kv_heads, dim, group, 16, dtype, seed=15)
+    g = torch.Generator(device=DEV).manual_seed(15)
+    k, v = torch.randn(2, kv, kv_heads, dim, generator=g, device=DEV).unbind(0)
+    v *= 2.0**-10
+    if where == "later":
+        v[100:] *= 2.0**22
+    elif where == "one_later":
+        v[90] *= 2.0**22
+        v[200, 1] *= 2.0**22
+    elif where == "behind":
+        window = 50
+        v[:81] *= 2.0**22
+    elif where == "zeros":
+        v[::3] = 0
+    else:
+        v *= torch.exp2(torch.randint(-4, 21, (kv, kv_heads, 1), generator=g, device=DEV).float())
+    refill(c, k, v)
+    c.check(*c.run(window=window), window=window)
+    ok()
+
+
+def test_hidden_keys_of_a_long_prompt():
+    """Rows of a prompt of many tiles, split over CTAs and not, hold while the values of later
+    keys grow 2^22 times: each side is off by half a step of out, and by 2^-10 (p and v rounded,
+    the smaller terms below 2^-11) of the largest value."""
+    cut = 300
+    for kv, heads in ((1500, 2), (700, 80)):
+        c = Case([kv], [kv], heads, heads // 2, 128, 128, 32, BF16, seed=16)
+        g = torch.Generator(device=DEV).manual_seed(16)
+        k, v = torch.randn(2, kv, heads // 2, 128, generator=g, device=DEV).unbind(0)
+        v *= 2.0**-10
+        refill(c, k, v)
+        a, la = c.run()
+        v[cut:] *= 2.0**22
+        refill(c, k, v)
+        b, lb = c.run()
+        ok()
+        off = (a[:cut].double() - b[:cut].double()).abs()
+        limit = 2 * (2.0**-10 + 2.0**-11) * float(v[:cut].abs().max())
+        assert bool((off <= limit + 2.0**-7 * (a[:cut].double().abs() + limit)).all())
+        assert torch.allclose(la[:cut], lb[:cut], rtol=0, atol=1e-4)

@@ -4,19 +4,23 @@
 // A CTA (one per SM) takes 256 rows of one (request, KV head), as two tiles of 128, against
 // tiles of 128 keys:
 //     S_i = Q_i K^T          tcgen05.mma, both operands in shared memory, S_i in TMEM
-//     p   = 2^(S_i ks - m + 6),  l += p
-//     O_i += P_i V           P_i (binary16) from TMEM, O_i in TMEM
+//     p   = 2^(S_i ks + E - m + 6),  l += p 2^-E
+//     O_i += P_i (V 2^-E)    P_i (binary16) from TMEM, O_i in TMEM
 // Where a key's row has one scale, K is its codes less Z, exact in 16 bits, and the scale meets
 // the score in fp32 (ks = S_k scale log2(e)). With several, K is S_k (q - Z) as a sum of two
 // 16-bit numbers (15 bits in all, so the sum is exact) and the product runs twice; ks is then
 // one number for bf16. binary16 has no room for every S_k (q - Z): there each key has a power of
 // two of its own that brings its largest S_k into [2^11, 2^12), and ks is the key's again. (A
 // fixed 2^-4 had made S_k below 2^-10 binary16 subnormals: 0.3 % off at 2e-5, 0 at 2^-21.)
-// For bf16 results V is S_v (q - Z) 2^-E rounded once to binary16 (half a step is 2^-11,
+// For bf16 results V 2^-E is S_v 2^-E (q - Z) rounded once to binary16 (half a step is 2^-11,
 // an eighth of out's); for fp16 results that would show, so V stays exact: with one scale the
-// codes less Z, S_v 2^-E meeting p, with several a sum of two numbers as for K. E is the
-// exponent of the largest S_v so far: one number for all rows, which moves rarely (O is
-// rescaled then), so values of any magnitude keep their bits.
+// codes less Z, S_v 2^-E meeting p, with several a sum of two numbers as for K.
+// E joins the exponent of p, so m is the row's own largest S_i ks + E and values of any magnitude
+// keep their bits. Where the largest S_v of the tile's keys lie within 2^4 of each other (as
+// nearly everywhere) E is one number for the tile; else every key has its own, from shared
+// memory: a key that a row does not see, were its S_v ever so large, takes no bits from the
+// others. (One E for all tiles so far, as it was, made the values of a row subnormal where a
+// later key's were 2^18 as large.)
 // One thread owns a row: it reads its 128 scores from TMEM, and m moves (which rescales O_i in
 // TMEM) only when a score passes it by 2^8; the scores are read again then. Of the constants of
 // a key only ks comes from shared memory for every score: three of them (scale, logarithm
@@ -60,6 +64,8 @@ constexpr int kRowsCta = 2 * kM;
 constexpr int kThreads = 512;
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr float kLift = 6.0f, kHeadroom = 8.0f;  // p <= 2^14
+constexpr int kEach = 1 << 20;  // in place of a tile's E: every key has its own
+constexpr int kApart = 3;       // exponents of S_v within a tile of one E differ by this at most
 
 // Registers of a thread after the split: the launch gives every warpgroup 128, and the four
 // shares add up to the same.
@@ -84,7 +90,7 @@ struct Ctl {
   uint64_t o_full;
   int64_t scan[16];
   uint32_t there[4][4];  // which keys of a tile exist, by the ring of vec
-  int exponent[4];       // E of a tile, by the same ring
+  int exponent[4];       // E of a tile, or kEach, by the same ring
 
   int b, tile, head;  // this CTA's unit; b < 0: none
   uint32_t tmem_base;
@@ -101,7 +107,9 @@ struct Cfg {
   static constexpr int kVBufs = kSplitV ? 1 : 2;
   static constexpr int kQBytes = kM * D * 2;  // one Q tile
   static constexpr int kTBytes = kN * D * 2;  // one K tile, one V^T tile; hi and lo are two
-  static constexpr int kVecFloats = (kKeyScale ? kN : 0) + (kScaleP ? kN : 0);  // ks, S_v 2^-E
+  static constexpr int kTop = kScaleP ? 0 : 4;  // exponent of the largest S_v 2^-E
+  static constexpr int kSvAt = kKeyScale ? kN : 0, kEAt = kSvAt + (kScaleP ? kN : 0);
+  static constexpr int kVecFloats = kEAt + kN;  // ks, S_v 2^-E, E
   static constexpr int kRawK = kN * (D / 2 + 8 * G);  // K codes, K and V scale words of a tile
   static constexpr int kRawV = kN * (D / 2 + 4 * G);  // V codes, V scale words
   static constexpr int kSmem = 1024 + 2 * kQBytes + 4 * kTBytes + kRawK + kRawV +
@@ -238,9 +246,9 @@ __device__ __forceinline__ int request_tiles(const Kv4AttnArgs& a, int b) {
 }
 
 // One row's 128 scores: p = 2^(s ks + up) as binary16 pairs (times the key's value scale where
-// kSv), their sum, and the largest exponent. ks from shared memory where kKs, else `k1`.
-// kMask: only keys low < pos <= lim count that `there` has.
-template <bool kKs, bool kSv, bool kMask>
+// C::kScaleP), their sum, and the largest exponent. ks from shared memory where C::kKeyScale,
+// else `k1`. kMask: only keys low < pos <= lim count that `there` has.
+template <class C, bool kMask>
 __device__ __forceinline__ float row_pass(uint32_t t_s, uint32_t vs, float k1, float up, int pos0,
                                           int lim, int low, const uint32_t* there,
                                           uint32_t (&p)[kN / 64][32], float2& sum) {
@@ -257,7 +265,7 @@ __device__ __forceinline__ float row_pass(uint32_t t_s, uint32_t vs, float k1, f
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       float2 ka = k2, kb = k2;
-      if (kKs) {
+      if (C::kKeyScale) {
         const float4 ks = lds_f4(vs + (32 * c + 4 * q) * 4);
         ka = make_float2(ks.x, ks.y);
         kb = make_float2(ks.z, ks.w);
@@ -278,8 +286,8 @@ __device__ __forceinline__ float row_pass(uint32_t t_s, uint32_t vs, float k1, f
       float2 p1 = make_float2(ex2(s1.x), ex2(s1.y));
       sum = __fadd2_rn(p0, sum);
       sum = __fadd2_rn(p1, sum);
-      if (kSv) {
-        const float4 sv = lds_f4(vs + (kN + 32 * c + 4 * q) * 4);
+      if (C::kScaleP) {
+        const float4 sv = lds_f4(vs + (C::kSvAt + 32 * c + 4 * q) * 4);
         p0 = __fmul2_rn(p0, make_float2(sv.x, sv.y));
         p1 = __fmul2_rn(p1, make_float2(sv.z, sv.w));
       }
@@ -288,6 +296,63 @@ __device__ __forceinline__ float row_pass(uint32_t t_s, uint32_t vs, float k1, f
     }
   }
   return mx;
+}
+
+// The same where every key has its own E, without `p`: 32 scores at a time. The largest exponent
+// s ks + E first; then, m being settled, p = 2^(s ks + E + up) to TMEM in place of the scores (of
+// keys that have been read) and the sum of p 2^-E.
+template <class C, class F>
+__device__ __forceinline__ void own_exponents(uint32_t t_s, uint32_t vs, float k1, int c, F use) {
+  uint32_t v[32];
+  tmem_ld32(t_s + 32 * c, v);
+  tmem_wait_ld();
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    float4 ks = make_float4(k1, k1, k1, k1);
+    if (C::kKeyScale) ks = lds_f4(vs + (32 * c + 4 * q) * 4);
+    const float4 e = lds_f4(vs + (C::kEAt + 32 * c + 4 * q) * 4);
+    use(4 * q, fmaf(__uint_as_float(v[4 * q]), ks.x, e.x), e.x);
+    use(4 * q + 1, fmaf(__uint_as_float(v[4 * q + 1]), ks.y, e.y), e.y);
+    use(4 * q + 2, fmaf(__uint_as_float(v[4 * q + 2]), ks.z, e.z), e.z);
+    use(4 * q + 3, fmaf(__uint_as_float(v[4 * q + 3]), ks.w, e.w), e.w);
+  }
+}
+template <class C>
+__device__ __forceinline__ float own_max(uint32_t t_s, uint32_t vs, float k1, int pos0, int lim,
+                                         int low, const uint32_t* there) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < kN / 32; ++c) {
+    const uint32_t bits = there[c];
+    own_exponents<C>(t_s, vs, k1, c, [&](int i, float x, float) {
+      const int pos = pos0 + 32 * c + i;
+      if (pos <= lim && pos > low && ((bits >> i) & 1u)) mx = fmaxf(mx, x);
+    });
+  }
+  return mx;
+}
+template <class C>
+__device__ __forceinline__ float own_store(uint32_t t_s, uint32_t vs, float k1, float up, int pos0,
+                                           int lim, int low, const uint32_t* there) {
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < kN / 32; ++c) {
+    const uint32_t bits = there[c];
+    float h[32];
+    own_exponents<C>(t_s, vs, k1, c, [&](int i, float x, float e) {
+      const int pos = pos0 + 32 * c + i;
+      const float p = pos <= lim && pos > low && ((bits >> i) & 1u) ? ex2(x + up) : 0.0f;
+      sum = fmaf(p, ex2(-e), sum);
+      h[i] = p;
+      if (C::kScaleP) h[i] *= __uint_as_float(lds32(vs + (C::kSvAt + 32 * c + i) * 4));
+    });
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = half2_bits(h[2 * i], h[2 * i + 1]);
+    tmem_st16(t_s + 16 * c, w);
+    tmem_wait_st();
+  }
+  return sum;
 }
 
 // kJoin: units may be split. (A kernel of its own: with the choice at run time the loop of the
@@ -305,7 +370,7 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
   uint8_t* sV = sK + 2 * C::kTBytes;       // [2: as for K][2 atoms of 64 keys][D rows][128 B]
   uint8_t* rawK = sV + 2 * C::kTBytes;     // [128 rows of K codes][K scale words][V's]
   uint8_t* rawV = rawK + C::kRawK;         // [128 rows of V codes][V scale words]
-  float* vec = reinterpret_cast<float*>(rawV + C::kRawV);  // [4][ks, S_v 2^-E][128]
+  float* vec = reinterpret_cast<float*>(rawV + C::kRawV);  // [4][ks, S_v 2^-E, E][128]
   Ctl* ctl = reinterpret_cast<Ctl*>(vec + 4 * C::kVecFloats);
   // (broadcast, so that the compiler knows the roles' branches, and the operands of the MMAs,
   // to be the same for a whole warp)
@@ -458,7 +523,6 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
     const uint32_t t_o = t_row + 2 * kN + i * 128;
     const uint32_t vec_s = smem_u32(vec);
     float m = -INFINITY, l = 0.0f;
-    int exponent = 0;
     bool ok = true;
     auto rescale = [&](float f) {
 #pragma unroll
@@ -486,34 +550,39 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
       const bool safe = pos0 + kN <= safe_end && pos0 >= safe_begin &&
                         (there[0] & there[1] & there[2] & there[3]) == 0xFFFFFFFFu;
       const int e = ctl->exponent[j & 3];
-      if (e != exponent) {
-        if (j > 0) rescale(ex2(static_cast<float>(exponent - e)));
-        exponent = e;
-      }
-      uint32_t p[kN / 64][32];
-      float2 sum;
-      // two passes settle any scores that fp32 can tell apart; the bound ends it for others
-      for (int pass = 0; pass < 3; ++pass) {
-        const float ref = m == -INFINITY ? 0.0f : m;
-        const float mx =
-            safe ? row_pass<C::kKeyScale, C::kScaleP, false>(t_s, vs, a.scale_log2, kLift - ref,
-                                                             0, 0, 0, there, p, sum)
-                 : row_pass<C::kKeyScale, C::kScaleP, true>(t_s, vs, a.scale_log2, kLift - ref,
-                                                            pos0, lim,
-                                                            a.window > 0 ? lim - a.window : -1,
-                                                            there, p, sum);
-        // mx is relative to m: above kLift + kHeadroom m has to move (from -inf: always)
-        const bool over = m == -INFINITY ? mx > -INFINITY : mx > kLift + kHeadroom;
-        if (!__any_sync(0xffffffffu, over)) break;
-        const float to = fmaxf(m, ref + (mx - kLift));
+      const int low = a.window > 0 ? lim - a.window : -1;
+      // m moves to a row's largest exponent
+      auto move = [&](float to) {
         const float f = to == -INFINITY || m == to ? 1.0f : ex2(m - to);
         m = to;
         l *= f;
         if (j > 0) rescale(f);
-      }
-      l += sum.x + sum.y;
+      };
+      if (e != kEach) {
+        const float lift = kLift + static_cast<float>(e);
+        uint32_t p[kN / 64][32];
+        float2 sum;
+        // two passes settle any scores that fp32 can tell apart; the bound ends it for others
+        for (int pass = 0; pass < 3; ++pass) {
+          const float ref = m == -INFINITY ? 0.0f : m;
+          const float mx =
+              safe ? row_pass<C, false>(t_s, vs, a.scale_log2, lift - ref, 0, 0, 0, there, p, sum)
+                   : row_pass<C, true>(t_s, vs, a.scale_log2, lift - ref, pos0, lim, low, there, p,
+                                       sum);
+          // mx is relative to m: above kLift + kHeadroom m has to move (from -inf: always)
+          const bool over = m == -INFINITY ? mx > -INFINITY : mx > kLift + kHeadroom;
+          if (!__any_sync(0xffffffffu, over)) break;
+          move(fmaxf(m, ref + (mx - kLift)));
+        }
+        l += (sum.x + sum.y) * pow2(-e);
 #pragma unroll
-      for (int c = 0; c < kN / 64; ++c) tmem_st32(t_s + 32 * c, p[c]);
+        for (int c = 0; c < kN / 64; ++c) tmem_st32(t_s + 32 * c, p[c]);
+      } else {
+        const float mx = own_max<C>(t_s, vs, a.scale_log2, pos0, lim, low, there);
+        if (__any_sync(0xffffffffu, mx > m + kHeadroom)) move(fmaxf(m, mx));
+        l += own_store<C>(t_s, vs, a.scale_log2, kLift - (m == -INFINITY ? 0.0f : m), pos0, lim, low,
+                          there);
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -523,7 +592,6 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
     if (ok && wait_warp(&ctl->o_full, 0, ctl, a.status)) {
       tc_fence_after();
       if (kJoin && parts > 1) {
-        const float up = ex2(static_cast<float>(exponent));
         float* dst = reinterpret_cast<float*>(static_cast<JoinDesc*>(a.workspace) +
                                               gridDim.x / splits) +
                      blockIdx.x * part_floats(D);
@@ -535,13 +603,13 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
 #pragma unroll
           for (int q = 0; q < 32; q += 4)
             *reinterpret_cast<float4*>(dst + (i * kM + r) * D + 32 * c + q) =
-                make_float4(__uint_as_float(v[q]) * up, __uint_as_float(v[q + 1]) * up,
-                            __uint_as_float(v[q + 2]) * up, __uint_as_float(v[q + 3]) * up);
+                make_float4(__uint_as_float(v[q]), __uint_as_float(v[q + 1]),
+                            __uint_as_float(v[q + 2]), __uint_as_float(v[q + 3]));
         }
         dst[kRowsCta * D + i * kM + r] = m;
         dst[kRowsCta * (D + 1) + i * kM + r] = l;
       } else {
-        const float inv = l == 0.0f ? 0.0f : ex2(static_cast<float>(exponent)) / l;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         uint16_t* dst = a.out + static_cast<int64_t>(u.q0 + tok) * a.o_tok +
                         static_cast<int64_t>(h) * a.o_head;
 #pragma unroll
@@ -578,9 +646,6 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
     const uint32_t rk = smem_u32(rawK), rv = smem_u32(rawV);
     const uint32_t rk_sz = rk + kN * (D / 2), rk_szv = rk_sz + kN * 4 * G, rv_sz = rv + kN * (D / 2);
     const uint32_t sK0 = smem_u32(sK), sV0 = smem_u32(sV), vec0 = smem_u32(vec);
-    // E: S_v 2^-E stays below 2 where it meets p (p <= 2^14), below 2^12 where it meets 15
-    constexpr int kTop = C::kScaleP ? 0 : 4, kMost = C::kScaleP ? 0 : 11;
-    int exponent = -64;  // of no value
     for (int j = 0; j < u.nt; ++j) {
       const int kb = C::kKBufs == 2 ? j & 1 : 0, vb = C::kVBufs == 2 ? j & 1 : 0;
       if (!wait_warp(&ctl->rk_full, j & 1, ctl, a.status)) break;
@@ -590,26 +655,34 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
       // what lies where no key is may be anything: its scales and zero-points count as 0
       const uint32_t* there = ctl->there[j & 3];
       const bool k_there = (there[warp - 8] >> lane) & 1u;
-      // the tile's largest S_v, so E, before anything that uses it
+      // E of the tile, before anything that uses it: S_v 2^-E is below 2 where it meets p
+      // (p <= 2^14), below 2^5 where it meets the codes
+      int exponent;
       {
         const uint32_t four = there[lane >> 3] >> (4 * (lane & 7));
-        uint32_t y = 0;  // binary16 patterns >= 0 compare as integers
+        uint32_t top[4] = {0, 0, 0, 0};  // binary16 patterns >= 0 compare as integers
 #pragma unroll
         for (int i = 0; i < G; ++i) {  // G words of each of the lane's four keys
           const uint4 x = lds128(rk_szv + 16 * (G * lane + i));
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if ((four >> ((4 * i + q) / G)) & 1u) y = max(y, w[q] & 0xFFFFu);
+            top[(4 * i + q) / G] = max(top[(4 * i + q) / G], w[q] & 0xFFFFu);
         }
-        y = __reduce_max_sync(0xffffffffu, y);  // alike in the four warps
-        if (y != 0) {
-          const int top = half_exponent(y);
-          if (top - exponent > kMost) exponent = top - kTop;
-        }
-        if (e == 0) ctl->exponent[j & 3] = exponent < -60 ? 0 : exponent;
+        uint32_t most = 0, least = 0x7C00u;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if ((four >> q) & 1u) {
+            most = max(most, top[q]);
+            least = min(least, top[q]);
+          }
+        most = __reduce_max_sync(0xffffffffu, most);  // alike in the four warps
+        least = __reduce_min_sync(0xffffffffu, least);
+        exponent = half_exponent(most) - C::kTop;
+        if (half_exponent(most) - half_exponent(least) > kApart) exponent = kEach;
+        if (e == 0) ctl->exponent[j & 3] = exponent;
       }
-      const float down = exponent < -60 ? 0.0f : ex2(static_cast<float>(-exponent));
+      const float down = exponent == kEach ? 0.0f : pow2(-exponent);
       {
         uint32_t words[G], zz[G], zh[G], sh[G], sl[G];
         uint32_t top = 0;
@@ -681,9 +754,14 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
         }
         const uint32_t vs = vec0 + (j & 3) * C::kVecFloats * 4 + e * 4;
         if (C::kKeyScale) sts_f32(vs, ks * a.scale_log2);
-        if (C::kScaleP) {
-          const uint32_t sv = k_there ? lds32(rk_szv + 4 * e) : 0u;
-          sts_f32(vs + kN * 4, f16_bits_to_f32(sv & 0xFFFFu) * down);
+        if (C::kScaleP || exponent == kEach) {
+          uint32_t sv = 0;
+#pragma unroll
+          for (int i = 0; i < G; ++i)
+            if (k_there) sv = max(sv, lds32(rk_szv + 4 * (G * e + i)) & 0xFFFFu);
+          const int own = exponent == kEach ? half_exponent(sv) - C::kTop : exponent;
+          if (C::kScaleP) sts_f32(vs + C::kSvAt * 4, f16_bits_to_f32(sv) * pow2(-own));
+          if (exponent == kEach) sts_f32(vs + C::kEAt * 4, static_cast<float>(own));
         }
         fence_async_smem();
         __syncwarp();
@@ -714,20 +792,32 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
         const uint32_t eight = there[vo >> 2] >> (8 * (vo & 3));
         uint32_t zz[G][4], zh[G][4], sv[G][4];
 #pragma unroll
-        for (int i = 0; i < G; ++i)
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w0[G], w1[G], top0 = 0, top1 = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w0 = lds32(rv_sz + 4 * (G * (8 * vo + 2 * k) + i));
-            uint32_t w1 = lds32(rv_sz + 4 * (G * (8 * vo + 2 * k + 1) + i));
-            if (!((eight >> (2 * k)) & 1u)) w0 = 0;
-            if (!((eight >> (2 * k + 1)) & 1u)) w1 = 0;
-            const uint32_t z2 = __byte_perm(w0, w1, 0x7632);
+          for (int i = 0; i < G; ++i) {
+            w0[i] = lds32(rv_sz + 4 * (G * (8 * vo + 2 * k) + i));
+            w1[i] = lds32(rv_sz + 4 * (G * (8 * vo + 2 * k + 1) + i));
+            if (!((eight >> (2 * k)) & 1u)) w0[i] = 0;
+            if (!((eight >> (2 * k + 1)) & 1u)) w1[i] = 0;
+            top0 = max(top0, w0[i] & 0xFFFFu);
+            top1 = max(top1, w1[i] & 0xFFFFu);
+          }
+          float d0 = down, d1 = down;
+          if (!C::kScaleP && exponent == kEach) {
+            d0 = pow2(C::kTop - half_exponent(top0));
+            d1 = pow2(C::kTop - half_exponent(top1));
+          }
+#pragma unroll
+          for (int i = 0; i < G; ++i) {
+            const uint32_t z2 = __byte_perm(w0[i], w1[i], 0x7632);
             zz[i][k] = hfma2(z2, 0x3C003C00u, 0x64006400u);
             zh[i][k] = hfma2(z2, 0xBC00BC00u, 0xD400D400u);
             if (!C::kScaleP)
-              sv[i][k] = half2_bits(f16_bits_to_f32(w0 & 0xFFFFu) * down,
-                                    f16_bits_to_f32(w1 & 0xFFFFu) * down);
+              sv[i][k] = half2_bits(f16_bits_to_f32(w0[i] & 0xFFFFu) * d0,
+                                    f16_bits_to_f32(w1[i] & 0xFFFFu) * d1);
           }
+        }
         const uint32_t dst = sV0 + vb * C::kTBytes + (vo >> 3) * (D * 128);
 #pragma unroll
         for (int n = 0; n < VB; ++n) {  // byte n: dimensions 16 n + 2 vg (low nibble), + 1
