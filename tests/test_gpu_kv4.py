@@ -819,3 +819,15 @@ def test_hidden_keys_of_a_long_prompt():
         limit = 2 * (2.0**-10 + 2.0**-11) * float(v[:cut].abs().max())
         assert bool((off <= limit + 2.0**-7 * (a[:cut].double().abs() + limit)).all())
         assert torch.allclose(la[:cut], lb[:cut], rtol=0, atol=1e-4)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1], [40, 40]])
+@pytest.mark.parametrize("entry", [-1, -2, -(1 << 31), 1 << 20, (1 << 31) - 1, "blocks"])
+def test_each_bad_entry_is_reported(q_lens, entry):
+    """One needed table entry outside the cache, the first number past it among them."""
+    c = Case([100, 90], q_lens, 8, 2, 128, 128, 16, BF16, seed=17)
+    c.run()
+    ok()
+    c.tables[1, 3] = c.cache.shape[0] if entry == "blocks" else entry
+    out, lse = c.run()
+    assert wq.wq_get_status() == RANGE and bool(torch.isfinite(out).all())

@@ -934,11 +934,11 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
       const int piece = 1 << plog, pieces = kN >> plog;
       const int64_t codes = static_cast<int64_t>(kc.block) * (D / 2);
       const int32_t* table = a.tables + b * a.ld_tables;
-      auto block_of = [&](int j) -> int {  // -1: no keys, -2: keys that the table does not reach
-        const int64_t pos = static_cast<int64_t>(u.t0 + j) * kN + lane * piece;
-        if (lane >= pieces || pos >= u.kv) return -1;
-        const int64_t place = pos >> kc.block_log2;
-        return place < a.width ? __ldg(table + place) : -2;
+      auto pos_of = [&](int j) { return static_cast<int64_t>(u.t0 + j) * kN + lane * piece; };
+      auto needed = [&](int64_t pos) { return lane < pieces && pos < u.kv; };
+      auto block_of = [&](int j) -> int {  // -1 too where the table does not reach
+        const int64_t place = pos_of(j) >> kc.block_log2;
+        return needed(pos_of(j)) && place < a.width ? __ldg(table + place) : -1;
       };
       int next = block_of(0), j = 0;
       bool ok = true;
@@ -946,9 +946,9 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
         const int blk = next;
         if (j + 1 < u.nt) next = block_of(j + 1);
         const bool good = blk >= 0 && blk < kc.num_blocks;
-        if (!good && blk != -1) set_status(a.status, kStRange);
+        const int64_t pos = pos_of(j);
+        if (!good && needed(pos)) set_status(a.status, kStRange);
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, good));
-        const int64_t pos = static_cast<int64_t>(u.t0 + j) * kN + lane * piece;
         const int at = static_cast<int>(pos & (kc.block - 1));
         const uint8_t* src =
             kc.data + (static_cast<int64_t>(good ? blk : 0) * kc.kv_heads + head) * kc.chunk_bytes();
