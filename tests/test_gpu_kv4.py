@@ -831,3 +831,25 @@ def test_each_bad_entry_is_reported(q_lens, entry):
     c.tables[1, 3] = c.cache.shape[0] if entry == "blocks" else entry
     out, lse = c.run()
     assert wq.wq_get_status() == RANGE and bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("block", [16, 64, 128, 256])
+@pytest.mark.parametrize("q_lens", [[1, 3], [40, 1], [300, 70]])
+@pytest.mark.parametrize("causal,window", [(True, 1), (True, 37), (True, 200), (False, 50)])
+def test_blocks_behind_the_window_may_be_gone(block, q_lens, causal, window):
+    """A server gives back the blocks that no later row sees: their table entries are not read.
+    An entry that is needed is still reported."""
+    c = Case([700, 523], q_lens, 8, 2, 128, 64, block, F16, seed=block)
+    c.check(*c.run(causal=causal, window=window), causal=causal, window=window)
+    tab = c.tables.clone()
+    for b, n in enumerate(q_lens):
+        first = max(0, c.kv_lens[b] - (n - 1 if causal else 0) - window)
+        tab[b, : first // block] = -1
+        tab[b, : first // block: 2] = 1 << 20
+    c.tables = tab
+    c.check(*c.run(causal=causal, window=window), causal=causal, window=window)
+    ok()
+    first = max(0, c.kv_lens[1] - (q_lens[1] - 1 if causal else 0) - window)
+    tab[1, first // block] = -1
+    c.run(causal=causal, window=window)
+    assert wq.wq_get_status() == RANGE

@@ -699,8 +699,8 @@ def wq_kv4_attention(Q, cache, tables, q_starts, kv_lens, max_q: int, group: int
     q_starts[b] .. q_starts[b + 1] - 1 are the last tokens of request b, whose kv_lens[b] tokens
     lie in the blocks of tables[b]. Returns out (Q's shape and type), or (out, lse float32
     [T, heads]). scale defaults to head_dim ** -0.5; max_q: the largest number of rows of a
-    request; window > 0: each row sees the last `window` keys only. Rows outside q_starts are
-    left as they were."""
+    request; window > 0: each row sees the last `window` keys only (table entries of blocks that
+    no row sees are not read). Rows outside q_starts are left as they were."""
     k = _KV4 or _kv4()
     handle = _kv4_stream(k, Q, stream)
     if handle.__class__ is not int:

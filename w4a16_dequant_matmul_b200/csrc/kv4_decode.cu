@@ -86,6 +86,7 @@ struct Cfg {
 struct Req {
   int q0, qn, kv;     // first row of Q, rows, keys
   int row_tiles, t0, nt;  // row tiles, first tile of keys, tiles
+  int first;              // first key that some row sees
   __device__ int64_t places(int kv_heads) const {
     return static_cast<int64_t>(kv_heads) * row_tiles * (nt + kUnitCost);
   }
@@ -129,6 +130,7 @@ __device__ __forceinline__ Req request(const Kv4AttnArgs& a, int b) {
     const int64_t f = static_cast<int64_t>(r.kv) - (a.causal ? r.qn - 1 : 0) - a.window;
     first = f > 0 ? static_cast<int>(f) : 0;
   }
+  r.first = first;
   r.t0 = first / kTile;
   // tiles that hold keys and that the table reaches (keys beyond it are left out)
   const int64_t reach = static_cast<int64_t>(a.width) << a.cache.block_log2;
@@ -385,7 +387,8 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
         const int64_t pos = static_cast<int64_t>(p0 + lane) << piece_log2;
         const int64_t place = pos >> kc.block_log2;
         cached = -1;
-        if (pos < r.kv && place < a.width) {
+        // (blocks that end before the first key seen may be gone: their entries are not read)
+        if (pos < r.kv && pos + piece > r.first && place < a.width) {
           cached = a.tables[b * a.ld_tables + place];
           if (cached < 0 || cached >= kc.num_blocks) {
             cached = -1;

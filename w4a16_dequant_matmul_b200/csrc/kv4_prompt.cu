@@ -217,6 +217,7 @@ __device__ __forceinline__ uint4 expand_k(uint32_t w, uint32_t zz, uint32_t zh) 
 struct Unit {
   int q0, rows, kv, row0;  // request's first row of Q, its rows and keys, the CTA's first row
   int shift;               // keys before the first query: row i sees keys up to shift + i / ratio
+  int first;               // first key that some row sees
   int t0, nt;              // first tile of 128 keys, number of tiles
 };
 
@@ -464,7 +465,8 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
     if (a.window > 0)
       first = (a.causal ? static_cast<int64_t>(u.shift) + u.row0 / a.ratio : u.kv - 1) - a.window + 1;
     if (first < 0) first = 0;
-    u.t0 = static_cast<int>(first / kN);
+    u.first = static_cast<int>(first);
+    u.t0 = u.first / kN;
     const int64_t last_tile = (end + kN - 1) / kN;
     u.nt = last_tile > u.t0 ? static_cast<int>(last_tile - u.t0) : 1;
     if (kJoin) {  // this CTA's share of the unit's tiles
@@ -935,7 +937,10 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
       const int64_t codes = static_cast<int64_t>(kc.block) * (D / 2);
       const int32_t* table = a.tables + b * a.ld_tables;
       auto pos_of = [&](int j) { return static_cast<int64_t>(u.t0 + j) * kN + lane * piece; };
-      auto needed = [&](int64_t pos) { return lane < pieces && pos < u.kv; };
+      // (blocks that end before the first key seen may be gone: their entries are not read)
+      auto needed = [&](int64_t pos) {
+        return lane < pieces && pos < u.kv && pos + piece > u.first;
+      };
       auto block_of = [&](int j) -> int {  // -1 too where the table does not reach
         const int64_t place = pos_of(j) >> kc.block_log2;
         return needed(pos_of(j)) && place < a.width ? __ldg(table + place) : -1;
