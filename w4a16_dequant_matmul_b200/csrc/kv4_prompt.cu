@@ -936,13 +936,13 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
       const int piece = 1 << plog, pieces = kN >> plog;
       const int64_t codes = static_cast<int64_t>(kc.block) * (D / 2);
       const int32_t* table = a.tables + b * a.ld_tables;
-      auto pos_of = [&](int j) { return static_cast<int64_t>(u.t0 + j) * kN + lane * piece; };
-      // (blocks that end before the first key seen may be gone: their entries are not read)
-      auto needed = [&](int64_t pos) {
-        return lane < pieces && pos < u.kv && pos + piece > u.first;
-      };
+      auto pos_of = [&](int j) { return (u.t0 + j) * kN + lane * piece; };  // <= 2^30 + a tile
+      // pieces that some row sees a key of: below `high`, above `low` (blocks that end before the
+      // first key seen may be gone: their entries are not read)
+      const int high = lane < pieces ? u.kv : 0, low = u.first - piece;
+      auto needed = [&](int pos) { return pos < high && pos > low; };
       auto block_of = [&](int j) -> int {  // -1 too where the table does not reach
-        const int64_t place = pos_of(j) >> kc.block_log2;
+        const int place = pos_of(j) >> kc.block_log2;
         return needed(pos_of(j)) && place < a.width ? __ldg(table + place) : -1;
       };
       int next = block_of(0), j = 0;
@@ -951,10 +951,16 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
         const int blk = next;
         if (j + 1 < u.nt) next = block_of(j + 1);
         const bool good = blk >= 0 && blk < kc.num_blocks;
-        const int64_t pos = pos_of(j);
+        const int pos = pos_of(j);
         if (!good && needed(pos)) set_status(a.status, kStRange);
-        const uint32_t n = __popc(__ballot_sync(0xffffffffu, good));
-        const int at = static_cast<int>(pos & (kc.block - 1));
+        const uint32_t copied = __ballot_sync(0xffffffffu, good), n = __popc(copied);
+        // the keys that exist, 32 a word: lanes 0 .. 3 (made ahead of the wait: behind it, key by
+        // key, they held up the copies, 649 us for the chunk above)
+        const int key = 32 * (lane & 3), left = u.kv - (u.t0 + j) * kN - key;
+        uint32_t bits = ((copied >> (key >> plog)) & 1u ? 0xFFFFu : 0u) |
+                        ((copied >> ((key + 16) >> plog)) & 1u ? 0xFFFF0000u : 0u);
+        bits &= left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
+        const int at = pos & (kc.block - 1);
         const uint8_t* src =
             kc.data + (static_cast<int64_t>(good ? blk : 0) * kc.kv_heads + head) * kc.chunk_bytes();
         const uint8_t* szk = src + 2 * codes + at * 4 * G;
@@ -963,20 +969,8 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
           ok = false;
           break;
         }
-        {  // the keys that exist, 32 a word: lanes 0 .. 3
-          const uint32_t ok_pieces = __ballot_sync(0xffffffffu, good);
-          if (lane < 4) {
-            uint32_t bits = 0;
-            for (int q = 0; q < 32; ++q) {
-              const int key = 32 * lane + q;
-              if (((ok_pieces >> (key >> plog)) & 1u) &&
-                  static_cast<int64_t>(u.t0 + j) * kN + key < u.kv)
-                bits |= 1u << q;
-            }
-            ctl->there[j & 3][lane] = bits;
-          }
-          __syncwarp();
-        }
+        if (lane < 4) ctl->there[j & 3][lane] = bits;
+        __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&ctl->rk_full, n * piece * (D / 2 + 8 * G));
         __syncwarp();
         if (good) {
