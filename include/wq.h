@@ -346,7 +346,8 @@ wq_status wq_kv4_read(const wq_kv4_cache* cache, const int32_t* slots, int64_t T
  * B at most 65536, lengths below 2^30. The workspace needs no initial contents; calls that may
  * run at the same time need one each. WQ_ERR_RANGE in the status word: a table entry outside
  * the cache, or a length beyond the table or 2^30, where it is needed (those keys are left
- * out). With a window, the entries of blocks that end before the first key that any of the
+ * out), or q_starts that descend or leave 0 .. T (of overlapping requests some rows may be left
+ * as they were). With a window, the entries of blocks that end before the first key that any of the
  * request's rows sees are not read: such blocks may have been given back. */
 typedef struct wq_kv4_attention_args {
   const uint16_t* Q;

@@ -853,3 +853,29 @@ def test_blocks_behind_the_window_may_be_gone(block, q_lens, causal, window):
     tab[1, first // block] = -1
     c.run(causal=causal, window=window)
     assert wq.wq_get_status() == RANGE
+
+
+@pytest.mark.parametrize("starts", [[0, 300, 0, 300], [0, 250, 200, 300], [-5, 100, 200, 300], [0, 100, 200, 301],
+                                    [300, 200, 100, 0], [0, 1 << 30, -(1 << 30), 300]])
+def test_row_starts_that_do_not_ascend_are_reported(starts):
+    """Whatever q_starts hold, rows inside Q are written or left, and the status says so."""
+    c = Case([400, 350, 330], [100, 100, 100], 8, 2, 128, 128, 32, BF16, seed=18)
+    c.run()
+    ok()
+    c.starts = ints(starts)
+    for max_q in (100, 0):
+        out, _ = c.run(max_q=max_q, out=torch.zeros_like(c.q))
+        assert wq.wq_get_status() == RANGE and bool(torch.isfinite(out).all())
+    one = wq.wq_kv4_attention(c.q, c.cache, c.tables[:1], ints([10, 5]), c.kv[:1], 100, out=torch.zeros_like(c.q))
+    assert wq.wq_get_status() == RANGE and not bool(one.any())
+
+
+def test_requests_may_leave_rows_between_them():
+    """Starts that ascend with the first above 0 and the last below T are no error."""
+    c = Case([400, 350], [100, 30], 8, 2, 128, 128, 32, BF16, seed=19)
+    want, _ = c.run()
+    q = torch.cat((c.q[:7] * 0, c.q, c.q[:9] * 0))
+    out = torch.full_like(q, 3.0)
+    wq.wq_kv4_attention(q, c.cache, c.tables, c.starts + 7, c.kv, 100, out=out)
+    ok()
+    assert torch.equal(out[7:-9], want) and bool((out[:7] == 3).all()) and bool((out[-9:] == 3).all())

@@ -97,6 +97,13 @@ struct Kv4AttnArgs {
   int most_rows;  // requests with more rows (tokens x ratio) than this go to the prompt kernel
   unsigned* status;
 };
+// Whether request b's rows lie in Q, behind those of the requests before it. (Rows of starts that
+// do not ascend could be more than Q has, and than the grid of the prompt kernel is made for.)
+__device__ __forceinline__ bool kv4_starts_ok(const Kv4AttnArgs& a, int64_t b) {
+  const int lo = a.q_starts[b], hi = a.q_starts[b + 1];
+  return lo >= 0 && hi >= lo && hi <= a.tokens;
+}
+
 size_t kv4_decode_workspace_bytes(int sms);
 cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int max_q, int sms, cudaStream_t st);
 

@@ -278,6 +278,7 @@ kv4_decode_kernel(const Kv4AttnArgs a) {
     for (int64_t b = r0; b < r0 + per && b < a.requests; ++b) {
       const Req r = request<kRows>(a, static_cast<int>(b));
       mine += r.places(a.cache.kv_heads);
+      if (blockIdx.x == 0 && !kv4_starts_ok(a, b)) set_status(a.status, kStRange);
     }
     int64_t incl = mine;
 #pragma unroll

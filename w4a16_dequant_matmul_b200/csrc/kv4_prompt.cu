@@ -382,8 +382,10 @@ kv4_prompt_kernel(const Kv4AttnArgs a, int splits_arg) {
     const int per = (a.requests + kThreads - 1) / kThreads;
     const int64_t r0 = static_cast<int64_t>(threadIdx.x) * per;
     int64_t mine = 0;
-    for (int64_t b = r0; b < r0 + per && b < a.requests; ++b)
+    for (int64_t b = r0; b < r0 + per && b < a.requests; ++b) {
       mine += static_cast<int64_t>(request_tiles(a, static_cast<int>(b))) * a.cache.kv_heads;
+      if (blockIdx.x == 0 && !kv4_starts_ok(a, b)) set_status(a.status, kStRange);
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
