@@ -343,7 +343,8 @@ wq_status wq_kv4_read(const wq_kv4_cache* cache, const int32_t* slots, int64_t T
  * number of rows of a request: it chooses kernels, and a wrong one costs time only.
  * Strides in elements, unit along head_dim, multiples of 8; Q, out, workspace 16-byte
  * aligned; Q and out bf16 or fp16; out may not overlap Q (the same pointer: WQ_ERR_UNSUPPORTED).
- * B at most 65536, lengths below 2^30. The workspace needs no initial contents; calls that may
+ * B at most 65536 (and, where max_q heads / kv_heads > 16, kv_heads B + T heads / 256 < 2^31),
+ * lengths below 2^30. The workspace needs no initial contents; calls that may
  * run at the same time need one each. WQ_ERR_RANGE in the status word: a table entry outside
  * the cache, or a length beyond the table or 2^30, where it is needed (those keys are left
  * out), or q_starts that descend or leave 0 .. T (of overlapping requests some rows may be left

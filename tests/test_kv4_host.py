@@ -301,3 +301,13 @@ def test_binding_allocates_on_the_given_stream(monkeypatch):
                                  ("attention", handle)]
     with pytest.raises(ValueError):  # a stream of another device
         calls(Stream(88, 1))
+
+
+def test_attention_grid_of_very_many_heads_and_requests(lib):
+    """kv_heads x B past the largest grid is refused where the prompt kernel would run."""
+    def f(kv_heads, B, mq):
+        c = cache(blocks=1, heads=kv_heads)
+        return lib.wq_kv4_attention(attention_args(c=c, heads=kv_heads, B=B, mq=mq), None)
+
+    assert f(65535, 65536, 17) == SHAPE and f(32768, 65536, 17) == SHAPE
+    assert f(65535, 65536, 16) not in (OK, SHAPE) and f(32767, 65536, 17) not in (OK, SHAPE)

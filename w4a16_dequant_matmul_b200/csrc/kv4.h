@@ -110,6 +110,9 @@ cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int max_q, int sms, cudaStre
 // Requests with more rows than a.most_rows, on tcgen05.
 constexpr int kKv4DecodeRows = 16;
 size_t kv4_prompt_workspace_bytes(int sms);
+// An upper bound of its (256 rows, KV head) units: the lengths are on the device, and CTAs without
+// a unit return. It is the kernel's grid, so at most 2^31 - 1.
+int64_t kv4_prompt_units(int64_t tokens, int64_t ratio, int64_t requests, int64_t kv_heads);
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs& a, int sms, cudaStream_t st);
 
 }  // namespace wq

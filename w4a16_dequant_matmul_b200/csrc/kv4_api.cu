@@ -161,6 +161,9 @@ wq_status wq_kv4_attention(const wq_kv4_attention_args* p, void* stream) {
     return WQ_ERR_SHAPE;
   // rows of a request are counted in 32 bits
   if (p->B > 65536 || p->T > kIntMax / p->heads || !count_ok(p->width)) return WQ_ERR_SHAPE;
+  const int32_t ratio = p->heads / c.kv_heads;
+  const bool prompts = static_cast<int64_t>(p->max_q) * ratio > wq::kKv4DecodeRows;
+  if (prompts && wq::kv4_prompt_units(p->T, ratio, p->B, c.kv_heads) > kIntMax) return WQ_ERR_SHAPE;
   if (p->Q == p->out) return WQ_ERR_UNSUPPORTED;  // CTAs that share a row read it at their own times
   if (!aligned(p->Q, 16) || !aligned(p->out, 16) || !aligned(p->lse, 4) ||
       !aligned(p->q_starts, 4) || !aligned(p->kv_lens, 4) || !aligned(p->tables, 4) ||
@@ -179,7 +182,7 @@ wq_status wq_kv4_attention(const wq_kv4_attention_args* p, void* stream) {
   a.bf16 = p->dtype == WQ_BF16;
   a.tokens = static_cast<int>(p->T);
   a.heads = p->heads;
-  a.ratio = p->heads / c.kv_heads;
+  a.ratio = ratio;
   a.q_tok = p->q_token_stride;
   a.q_head = p->q_head_stride;
   a.o_tok = p->o_token_stride;
@@ -203,7 +206,7 @@ wq_status wq_kv4_attention(const wq_kv4_attention_args* p, void* stream) {
   // kernel gets those requests and the decode kernel the others; which are which is read on
   // the device. A single request needs no such split.
   a.most_rows = static_cast<int>(kIntMax);
-  if (static_cast<int64_t>(p->max_q) * a.ratio > wq::kKv4DecodeRows) {
+  if (prompts) {
     a.most_rows = a.requests == 1 ? 0 : wq::kKv4DecodeRows;
     const wq_status e = from_cuda(wq::launch_kv4_prompt(a, sms, st));
     if (e != WQ_OK || a.requests == 1) return e;

@@ -1096,10 +1096,12 @@ size_t kv4_prompt_workspace_bytes(int sms) {
   return static_cast<size_t>(sms) * (sizeof(JoinDesc) + part_floats(128) * sizeof(float));
 }
 
+int64_t kv4_prompt_units(int64_t tokens, int64_t ratio, int64_t requests, int64_t kv_heads) {
+  return (tokens * ratio / kRowsCta + requests) * kv_heads;
+}
+
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs& a, int sms, cudaStream_t st) {
-  // an upper bound of the units: the lengths are on the device, CTAs without a unit return
-  const int64_t units = (static_cast<int64_t>(a.tokens) * a.ratio / kRowsCta + a.requests) *
-                        a.cache.kv_heads;
+  const int64_t units = kv4_prompt_units(a.tokens, a.ratio, a.requests, a.cache.kv_heads);
   // (units splits <= sms, for which the workspace is made)
   const int splits = units < sms ? static_cast<int>(sms / units) : 1;
   const int groups = a.cache.groups();
