@@ -879,3 +879,20 @@ def test_requests_may_leave_rows_between_them():
     wq.wq_kv4_attention(q, c.cache, c.tables, c.starts + 7, c.kv, 100, out=out)
     ok()
     assert torch.equal(out[7:-9], want) and bool((out[:7] == 3).all()) and bool((out[-9:] == 3).all())
+
+
+def test_block_tables_of_wild_lengths():
+    """Lengths near 2^31 of many requests: reported, what fits is right, and the call takes no
+    longer for them."""
+    B, n = 5000, (1 << 31) - 300
+    tab = torch.full((B, 4), -1, dtype=torch.int32, device=DEV)
+    args = (ints([0] * B), ints([n] * B), ints([5, 6, 7]), tab, 16, 100)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    slots, starts, kv, taken = wq.wq_kv4_block_tables(*args)
+    end.record()
+    assert wq.wq_get_status() == RANGE
+    assert start.elapsed_time(end) < 100
+    assert slots.tolist() == [16 * (5 + i // 16) + i % 16 for i in range(48)] + [-1] * 52
+    assert tab[0].tolist() == [5, 6, 7, -1] and bool((tab[1:] == -1).all()) and taken.item() == 3
+    assert starts[:3].tolist() == [0, n, (1 << 31) - 1] and bool((kv == n).all())

@@ -100,14 +100,15 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(Kv4TablesArgs
       }
       return l;
     };
-    // newly taken blocks, spread over the whole grid
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kTabThreads + t; i < tb;
+    // newly taken blocks, spread over the whole grid, as far as there are free ones (wild lengths
+    // would ask for 2^36 of them)
+    const int64_t there = a.n_free - blk0 < tb ? a.n_free - blk0 : tb;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kTabThreads + t; i < there;
          i += static_cast<int64_t>(gridDim.x) * kTabThreads) {
       const int k = find(s_blk, static_cast<int>(i));
       const int place = ((s_ctx[k] + bs - 1) >> a.block_log2) + static_cast<int>(i) - s_blk[k];
-      const int64_t f = blk0 + i;
-      if (place < a.width && f < a.n_free)
-        a.tables[(r0 + k) * a.ld_tables + place] = a.free_blocks[f];
+      if (place < a.width)
+        a.tables[(r0 + k) * a.ld_tables + place] = a.free_blocks[blk0 + i];
       else
         bad = true;
     }
