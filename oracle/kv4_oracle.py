@@ -78,10 +78,10 @@ def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None):
     the row, key *'s, the sum of p_j 2^-E_j is at least 2^(6 - E_*) l, and the error that key j
     brings into out at most 2^-31 |v_j| 2^(E_* - E_j) / l. |v_j| is at most 15 S_j, S_j the key's
     largest. Few rows have E = log2 S: 2^-31 15 S_*. For prompts S_j < 2^(E_j + 5), and keys of one
-    tile share E unless the exponents of their S differ by more than 3, so S_* >= 2^(E_* + 1):
-    2^-27 15 S_*; where S 2^-E meets p, S_j < 2^(E_j + 1) and S_* >= 2^(E_* - 3): the same. Where
+    tile share E unless the exponents of their S differ by more than 6, so S_* >= 2^(E_* - 2):
+    2^-24 15 S_*; where S 2^-E meets p, an error of 15 2^-25 and S_* >= 2^(E_* - 6): 2^-25. Where
     a rounded value S 2^-E (q - Z) of a prompt, or its S 2^-E, is a subnormal it errs by 15 2^-25,
-    with the key's largest S 2^-E at 2 at least: 2^-26 15 S. Only keys that the row sees come into
+    with the key's largest S 2^-E at 2^-2 at least: 2^-23 15 S. Only keys that the row sees come into
     this. 15 S <= 2.2 max_d |v_j| (the range 15 S lies within twice the largest stored value, each
     end of it within S/2), but S = 1 for a group of zeros, taken to be where 32 values are. For a
     masked row all of it is 0."""
@@ -111,7 +111,7 @@ def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None):
             rel = 2 * e + 2.0**-10 + 2.0**-20 + (kv / 16 + 64) * 2.0**-23
             zeros = (vv.reshape(len(vv), -1, min(32, dim)) == 0).all(-1).any()
             top = max(2.2 * np.abs(vv).max(), 15.0 if zeros else 0.0)  # 15 S of the keys seen
-            low = ((last + 1 - first) * 2.0**-27 / l + 2.0**-26) * top
+            low = ((last + 1 - first) * 2.0**-24 / l + 2.0**-23) * top
             bound[i, h] = rel * (p @ np.abs(vv) / l) + low
             bound_lse[i, h] = e + 2.0**-20 * (1 + abs(lse[i, h])) + (kv / 16 + 64) * 2.0**-23
     return out, lse, bound, bound_lse

@@ -772,11 +772,11 @@ def test_small_and_large_keys(dim, group, dtype, spread):
 
 @pytest.mark.parametrize("dim,group", SHAPES)
 @pytest.mark.parametrize("dtype", [BF16, F16])
-@pytest.mark.parametrize("where", ["later", "one_later", "behind", "zeros", "mixed"])
+@pytest.mark.parametrize("where", ["later", "one_later", "behind", "zeros", "mixed", "near"])
 def test_value_scales_that_a_row_does_not_see(dim, group, dtype, where):
     """Values 2^22 as large on keys that most rows of the tile do not see (later ones, one only,
     those behind the window) take no bits from the others; rows of zeros (S' = 1) and scales from
-    all over the range among small values."""
+    all over the range, or within 2^6, among small values."""
     kv, heads, kv_heads, window = 230, 4, 2, 0
     c = Case([kv], [kv if where in ("later", "one_later") else 100], heads, kv_heads, dim, group, 16, dtype, seed=15)
     g = torch.Generator(device=DEV).manual_seed(15)
@@ -792,6 +792,9 @@ def test_value_scales_that_a_row_does_not_see(dim, group, dtype, where):
         v[:81] *= 2.0**22
     elif where == "zeros":
         v[::3] = 0
+    elif where == "near":  # one exponent a tile, the key of most weight with the smallest values
+        v *= torch.exp2(torch.randint(0, 6, (kv, kv_heads, 1), generator=g, device=DEV).float())
+        k[5], v[5] = c.q[-1, ::2].float() * 2, v[5] * 2.0**-5
     else:
         v *= torch.exp2(torch.randint(-4, 21, (kv, kv_heads, 1), generator=g, device=DEV).float())
     refill(c, k, v)
