@@ -57,7 +57,8 @@ def kv4_block_tables(ctx, new, free, tables, block, n_slots):
     return tables, np.array(slots), np.array(starts), np.array(ctx) + np.array(new), at
 
 
-def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None):
+def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None,
+                  exact_values=False):
     """One request: q [n, heads, D], k and v [kv, kv_heads, D], float64. Returns (out, lse,
     bound_out, bound_lse): the formula's values, and how far a kernel may be from them before
     its output is rounded.
@@ -72,7 +73,9 @@ def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None):
     wrong by a relative
         e = ((D/8 + 8) 2^-23 31 + 2^-32) S scale sum|x|
     at most, and numerator and denominator by e each; with it 2^-11 for its rounding to binary16
-    (half a step) and 2^-11 for that of its value, 2^-20 for exp2, log2 and the scale products, and (kv/16 + 64) 2^-23 for the two fp32 sums over the keys. The error of out is
+    (half a step) and 2^-11 for that of its value (`exact_values`: none, as with few rows or fp16
+    results), 2^-20 for exp2, log2 and the scale products, and (kv/16 + 64) 2^-23 for the two fp32
+    sums over the keys. The error of out is
     that times sum_j p_j |v_j|. Where a rounded p is a binary16 subnormal it errs by half its
     step, 2^-25. With p_j = 2^(s_j + E_j - m + c), c >= 6, and m at most the largest s_j + E_j of
     the row, key *'s, the sum of p_j 2^-E_j is at least 2^(6 - E_*) l, and the error that key j
@@ -108,7 +111,7 @@ def kv4_attention(q, k, v, scale, causal=True, window=0, s_max=None):
             e = 0.0
             if s_max is not None:
                 e = ((dim / 8 + 8) * 2.0**-23 * 31 + 2.0**-32) * s_max * abs(scale) * np.abs(q[i, h]).sum()
-            rel = 2 * e + 2.0**-10 + 2.0**-20 + (kv / 16 + 64) * 2.0**-23
+            rel = 2 * e + (2.0**-11 if exact_values else 2.0**-10) + 2.0**-20 + (kv / 16 + 64) * 2.0**-23
             zeros = (vv.reshape(len(vv), -1, min(32, dim)) == 0).all(-1).any()
             top = max(2.2 * np.abs(vv).max(), 15.0 if zeros else 0.0)  # 15 S of the keys seen
             low = ((last + 1 - first) * 2.0**-24 / l + 2.0**-23) * top

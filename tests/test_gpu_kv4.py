@@ -899,3 +899,32 @@ def test_block_tables_of_wild_lengths():
     assert slots.tolist() == [16 * (5 + i // 16) + i % 16 for i in range(48)] + [-1] * 52
     assert tab[0].tolist() == [5, 6, 7, -1] and bool((tab[1:] == -1).all()) and taken.item() == 3
     assert starts[:3].tolist() == [0, n, (1 << 31) - 1] and bool((kv == n).all())
+
+
+@pytest.mark.parametrize("dim,group", SHAPES)
+@pytest.mark.parametrize("dtype,q_lens", [(BF16, [1, 2]), (F16, [1, 2]), (F16, [90, 1])])
+def test_values_are_exact(dim, group, dtype, q_lens):
+    """Few rows, and fp16 results: of the two operands of the second product only the
+    probabilities are rounded."""
+    c = Case([300, 77], q_lens, 8, 2, dim, group, 64, dtype, seed=20)
+    out, lse = c.run()
+    ok()
+    half_step, at = torch.finfo(dtype).eps / 2, 0
+    tiny = float(torch.finfo(dtype).smallest_normal) * half_step
+    for b, n in enumerate(q_lens):
+        q = c.q[at: at + n].double().cpu().numpy()
+        want, _, bound, _ = oracle.kv4_attention(q, c.k[b], c.v[b], dim**-0.5, s_max=c.smax[b], exact_values=True)
+        got = out[at: at + n].double().cpu().numpy()
+        assert (np.abs(got - want) <= bound + (np.abs(want) + bound) * half_step + tiny).all()
+        at += n
+
+
+@pytest.mark.parametrize("dim,group", SHAPES)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("block", [128, 256])
+def test_prompts_over_large_blocks(dim, group, dtype, block):
+    """Blocks of one tile and of two, the last one ragged in either half."""
+    c = Case([700, 380, 129], [60, 150, 129], 8, 2, dim, group, block, dtype, seed=block)
+    c.check(*c.run())
+    c.check(*c.run(causal=False, window=300), causal=False, window=300)
+    ok()
