@@ -928,3 +928,32 @@ def test_prompts_over_large_blocks(dim, group, dtype, block):
     c.check(*c.run())
     c.check(*c.run(causal=False, window=300), causal=False, window=300)
     ok()
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(300, 1), (130, 2), (256, 1)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_very_many_query_heads_a_kv_head(heads, kv_heads, dtype):
+    """A token's rows pass a row tile, and several; as prompts and on the kernel for few rows."""
+    c = Case([150, 40], [1, 2], heads, kv_heads, 64, 32, 16, dtype, seed=21)
+    for max_q in (2, 0):
+        c.check(*c.run(max_q=max_q))
+    ok()
+
+
+def test_prompts_among_many_requests():
+    """More requests than threads of either kernel, a few of them prompts."""
+    rng = np.random.default_rng(1)
+    q_lens = np.ones(600, int)
+    q_lens[[3, 511, 512, 599]] = 40, 70, 0, 33
+    c = Case((q_lens + rng.integers(0, 50, 600)).tolist(), q_lens.tolist(), 8, 2, 64, 64, 16, BF16, seed=22)
+    c.check(*c.run())
+    ok()
+
+
+def test_requests_without_rows_only():
+    c = Case([30, 0, 7], [1, 0, 0], 8, 2, 64, 64, 16, BF16, seed=23)
+    for max_q in (1, 100):
+        out = torch.full_like(c.q, 5.0)
+        wq.wq_kv4_attention(c.q, c.cache, c.tables, c.starts * 0, c.kv, max_q, out=out)
+        ok()
+        assert bool((out == 5).all())
