@@ -295,7 +295,7 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 // Codes are clipped only in warps with a group whose end codes leave [0, 15], as there (rare: a
 // tie at both ends, or a subnormal S').
 // Bytes: 2 an element in, D/2 + 4 D/g a row out: 16384 tokens of 8 heads of 128 in 20.9 us, 4.1
-// TB/s (50 us with a word a lane; 22.9 with every code clipped, 25 if two rows a lane share the
+// TB/s; 69 % of the issue slots, so bound by instructions as much as by memory (50 us with a word a lane; 22.9 with every code clipped, 25 if two rows a lane share the
 // decisions too).
 template <int D, int G, bool kBf16, bool kV>
 __device__ __forceinline__ void append_rows(const Kv4AppendArgs& a) {
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(Kv4AppendArgs a) {
 
 // The inverse, with the lanes and words of the append: values S'(q - Z), exact in fp32, or
 // rounded once to 16 bits; slot < 0 gives zeros. The slots of the next rows are loaded ahead.
-// Bound by HBM: 16384 tokens of 8 heads of 128 to fp32 in 29 us, 5.2 TB/s (39 us with a word a
+// Bound by HBM: 16384 tokens of 8 heads of 128 to fp32 in 29 us, 5.3 TB/s (39 us with a word a
 // lane; 51 us where each lane stores its own 32 bytes in two halves), to 16 bits in 17 us.
 template <int D, int G, int kOut, bool kV>  // kOut: WQ_F32, WQ_BF16, WQ_F16
 __device__ __forceinline__ void read_rows(const Kv4ReadArgs& a) {

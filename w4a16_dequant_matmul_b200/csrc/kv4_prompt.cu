@@ -26,13 +26,14 @@
 // a key only ks comes from shared memory for every score: three of them (scale, logarithm
 // and reciprocal of S_v) cost 10 % more.
 //
-// Measured: 1024 new tokens behind 15360 cached ones, 64 query and 8 KV heads of 128: 607 us,
-// 877 TFLOP/s; 2.4 us for a step of 128 keys, whose products take 1.1 us of the tensor core at
+// Measured: 1024 new tokens behind 15360 cached ones, 64 query and 8 KV heads of 128: 604 us,
+// 881 TFLOP/s; 2.4 us for a step of 128 keys, whose products take 1.1 us of the tensor core at
 // 1.8 GHz and whose powers as long of the exponential unit. A row tile's softmax and its products
 // take turns, and the two tiles overlap each other's only in part: that latency chain is what
 // bounds the loop, not one unit. Dropped, each slower: score products of half a tile with two in
 // flight (they read the query tile from shared memory twice as often, 740 us), polling waits,
-// more registers for the softmax.
+// more registers for the softmax. (All forms spill, 48 to 300 bytes a thread, for the most part
+// around the softmax loop and in the expansion of several scales.)
 //
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (and Q's load, the output); 8-11 expand the codes
 // into the two-deep rings of K (rows = keys) and V^T (rows = dimensions, built from octets of
