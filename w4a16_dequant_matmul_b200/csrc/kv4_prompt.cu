@@ -32,7 +32,7 @@
 // take turns, and the two tiles overlap each other's only in part: that latency chain is what
 // bounds the loop, not one unit. Dropped, each slower: score products of half a tile with two in
 // flight (they read the query tile from shared memory twice as often, 740 us), polling waits,
-// more registers for the softmax. (All forms spill, 48 to 300 bytes a thread, for the most part
+// more registers for the softmax. (All forms spill, 20 to 150 bytes a thread, for the most part
 // around the softmax loop and in the expansion of several scales.)
 //
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (and Q's load, the output); 8-11 expand the codes
@@ -53,6 +53,8 @@
 
 #include "common.cuh"
 #include "kv4.h"
+#include "kv4_math.cuh"
+#include "mma_frag.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 
@@ -134,34 +136,10 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* c
   return ok;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
 __device__ __forceinline__ uint32_t bsub2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
-}
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
@@ -177,16 +155,6 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
